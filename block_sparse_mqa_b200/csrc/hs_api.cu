@@ -167,7 +167,7 @@ hs_status check_score_args(const void* q, int64_t qrs, int64_t qhs, const void* 
 
 extern "C" {
 
-int hs_version(void) { return 300; }
+int hs_version(void) { return 400; }
 
 const char* hs_status_string(hs_status s) {
   switch (s) {
@@ -206,6 +206,9 @@ int hs_path(int op, hs_dtype dtype, int num_heads, int dk, int dv, int block_siz
           hs::tc_block_score_supported(num_heads, dk, block_size, 0))
         return HS_PATH_TCGEN05;
       return HS_PATH_SIMT;
+    case HS_OP_SWA_FIRST_MQA:
+    case HS_OP_SWA_FIRST_MQA_BWD:
+    case HS_OP_KV4_MQA_DECODE: return HS_PATH_SIMT;
     case HS_OP_SPARSE_MQA_BWD:
     case HS_OP_SWA_MQA_BWD:
       if (!g_force_simt.load() && hs::tc_backward_shape_ok(dtype, num_heads, dk, dv))
@@ -225,8 +228,12 @@ int hs_path(int op, hs_dtype dtype, int num_heads, int dk, int dv, int block_siz
 
 size_t hs_workspace_size(int op, int total_tokens, int num_docs, int max_seqlen, int num_heads,
                          int dk, int dv, hs_dtype dtype, int block_size) {
-  if ((op == HS_OP_SPARSE_MQA_BWD || op == HS_OP_SWA_MQA_BWD) && total_tokens > 0 &&
-      num_heads > 0)
+  if (op == HS_OP_KV4_MQA_DECODE) {  // total_tokens = the number of sequences
+    if (total_tokens <= 0 || num_heads <= 0 || dv <= 0) return 0;
+    return hs::simt_kv4_decode_workspace(total_tokens, num_heads, max_seqlen, dv);
+  }
+  if ((op == HS_OP_SPARSE_MQA_BWD || op == HS_OP_SWA_MQA_BWD || op == HS_OP_SWA_FIRST_MQA_BWD) &&
+      total_tokens > 0 && num_heads > 0)
     return bwd_workspace(total_tokens, num_heads, dk, dv, dtype);
   if ((op != HS_OP_BLOCK_SCORE && op != HS_OP_BLOCK_SCORE_ATTN) || total_tokens <= 0 ||
       !valid_block(block_size))
@@ -359,7 +366,7 @@ static hs_status attention_common(hs::AttnArgs& a, bool sparse, const void* q, i
   if (total_tokens == 0) return HS_OK;
   r = status_ptr(&a.p.status);
   if (r != HS_OK) return r;
-  const bool tc = dtype == HS_BF16 && !g_force_simt.load() &&
+  const bool tc = dtype == HS_BF16 && !g_force_simt.load() && !a.with_first &&
                   hs::tc_attention_supported(num_heads, dk, dv, a.block_size, sparse) &&
                   hs::tc_attention_eligible(a);
   if (tc) return launched_on(hs::launch_tc_attention(a, sparse, g_wait_limit.load(), stream),
@@ -538,8 +545,8 @@ static hs_status backward_common(hs::BwdArgs& a, bool sparse, const void* q, int
                                  int64_t vrs, const int32_t* cu, int num_docs, int total_tokens,
                                  int max_seqlen, int num_heads, int dk, int dv, hs_dtype dtype,
                                  float scale, const float* sink, const void* out,
-                                 const float* lse, const void* dout, float* dq, float* dkey,
-                                 float* dval, float* dsink, void* workspace,
+                                 const float* lse, const void* dout, void* dq, void* dkey,
+                                 void* dval, float* dsink, void* workspace,
                                  size_t workspace_bytes, hs_stream_t stream) {
   hs_status r = check_problem(a.p, q, qrs, qhs, k, krs, cu, num_docs, total_tokens, max_seqlen,
                               num_heads, dk, dv, dtype, scale);
@@ -618,6 +625,249 @@ hs_status hs_swa_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_head_str
                          v_row_stride, cu_seqlens, num_docs, total_tokens, max_seqlen, num_heads,
                          dk, dv, dtype, softmax_scale, sink, out, lse, dout, dq, dkey, dval,
                          dsink, workspace, workspace_bytes, stream);
+}
+
+// Window and first tokens beyond every document change nothing; clamped so
+// that sums of token indices stay far from the 32-bit limit.
+static hs_status check_window_first(int& window, int& num_first, int total_tokens) {
+  if (window < 1) return fail(HS_ERR_INVALID_ARG, "window %d < 1", window);
+  if (num_first < 0) return fail(HS_ERR_INVALID_ARG, "num_first %d < 0", num_first);
+  const int most = total_tokens > 1 ? total_tokens : 1;
+  if (window > most) window = most;
+  if (num_first > most) num_first = most;
+  return HS_OK;
+}
+
+hs_status hs_swa_first_mqa_fwd(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                               const void* k, int64_t k_row_stride, const void* v,
+                               int64_t v_row_stride, const int32_t* cu_seqlens, int num_docs,
+                               int total_tokens, int max_seqlen, int num_heads, int dk, int dv,
+                               hs_dtype dtype, float softmax_scale, int window, int num_first,
+                               const float* sink, void* out, float* lse, hs_stream_t stream) {
+  hs_status r = check_window_first(window, num_first, total_tokens);
+  if (r != HS_OK) return r;
+  hs::AttnArgs a{};
+  a.block_size = 64;  // plays no part
+  a.window = window;
+  a.first = num_first;
+  a.with_first = true;
+  return attention_common(a, false, q, q_row_stride, q_head_stride, k, k_row_stride, v,
+                          v_row_stride, cu_seqlens, num_docs, total_tokens, max_seqlen,
+                          num_heads, dk, dv, dtype, softmax_scale, sink, out, lse, stream);
+}
+
+hs_status hs_swa_first_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                               const void* k, int64_t k_row_stride, const void* v,
+                               int64_t v_row_stride, const int32_t* cu_seqlens, int num_docs,
+                               int total_tokens, int max_seqlen, int num_heads, int dk, int dv,
+                               hs_dtype dtype, float softmax_scale, int window, int num_first,
+                               const float* sink, const void* out, const float* lse,
+                               const void* dout, void* dq, void* dkey, void* dval, float* dsink,
+                               void* workspace, size_t workspace_bytes, hs_stream_t stream) {
+  hs_status r = check_window_first(window, num_first, total_tokens);
+  if (r != HS_OK) return r;
+  // no tokens: the sink's gradient is the one output that still has elements
+  if (total_tokens == 0 && sink && dsink && num_heads >= 1 && num_heads <= kMaxHeads) {
+    const cudaError_t e = cudaMemsetAsync(dsink, 0, sizeof(float) * num_heads, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+  }
+  hs::BwdArgs a{};
+  a.block_size = 64;
+  a.window = window;
+  a.first = num_first;
+  a.grad_like_input = true;
+  return backward_common(a, false, q, q_row_stride, q_head_stride, k, k_row_stride, v,
+                         v_row_stride, cu_seqlens, num_docs, total_tokens, max_seqlen, num_heads,
+                         dk, dv, dtype, softmax_scale, sink, out, lse, dout, dq, dkey, dval,
+                         dsink, workspace, workspace_bytes, stream);
+}
+
+// ------------------------------------------------------------ 4-bit cache
+
+static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+static int log2_of(int v) {
+  int n = 0;
+  while ((1 << n) < v) ++n;
+  return n;
+}
+
+// Checks of the page geometry shared by the cache calls.
+static hs_status check_pages(const int32_t* block_table, int64_t table_stride, int table_width,
+                             int num_pages, int page_size, int num_seqs) {
+  if (!valid_block(page_size))
+    return fail(HS_ERR_UNSUPPORTED, "page_size %d not in {16, 32, 64, 128}", page_size);
+  if (num_pages < 0 || num_seqs < 0) return fail(HS_ERR_INVALID_ARG, "negative size");
+  if (!block_table) return fail(HS_ERR_INVALID_ARG, "block_table is NULL");
+  if (table_width < 1) return fail(HS_ERR_INVALID_ARG, "table_width %d < 1", table_width);
+  if (table_stride < table_width)
+    return fail(HS_ERR_INVALID_ARG, "table_stride %lld < table_width", (long long)table_stride);
+  return HS_OK;
+}
+
+static hs_status check_width(const char* name, int width) {
+  if (width < 32 || width > kMaxDim || width % 32 != 0)
+    return fail(HS_ERR_UNSUPPORTED, "%s %d is not a multiple of 32 in [32, %d]", name, width,
+                kMaxDim);
+  return HS_OK;
+}
+
+static hs_status check_dtype(hs_dtype dtype) {
+  if (dtype != HS_F32 && dtype != HS_BF16) return fail(HS_ERR_UNSUPPORTED, "dtype %d", (int)dtype);
+  return HS_OK;
+}
+
+size_t hs_kv4_page_bytes(int width, int page_size) {
+  if (width < 32 || width > kMaxDim || width % 32 != 0 || !valid_block(page_size)) return 0;
+  const int g = width / 32;
+  return (size_t)page_size * (16 * g + 4 * ((g + 3) / 4));
+}
+
+static hs_status check_rows(hs::Kv4Rows& a, const int32_t* block_table, int64_t table_stride,
+                            int table_width, int num_pages, int page_size,
+                            const int32_t* cu_seqlens, const int32_t* seq_lens, int num_seqs,
+                            int total_tokens) {
+  hs_status r =
+      check_pages(block_table, table_stride, table_width, num_pages, page_size, num_seqs);
+  if (r != HS_OK) return r;
+  if (total_tokens < 0) return fail(HS_ERR_INVALID_ARG, "total_tokens < 0");
+  if (total_tokens > 0 && num_seqs < 1)
+    return fail(HS_ERR_INVALID_ARG, "num_seqs must be >= 1 when total_tokens > 0");
+  if (!cu_seqlens || !seq_lens) return fail(HS_ERR_INVALID_ARG, "cu_seqlens or seq_lens is NULL");
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.table_width = table_width;
+  a.num_pages = num_pages;
+  a.ps_log2 = log2_of(page_size);
+  a.cu = cu_seqlens;
+  a.seq_lens = seq_lens;
+  a.num_seqs = num_seqs;
+  a.total_tokens = total_tokens;
+  return HS_OK;
+}
+
+hs_status hs_kv4_append(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                        void* k_cache, void* v_cache, const int32_t* block_table,
+                        int64_t table_stride, int table_width, int num_pages, int page_size,
+                        const int32_t* cu_seqlens, const int32_t* seq_lens, int num_seqs,
+                        int total_tokens, int dk, int dv, hs_dtype dtype, hs_stream_t stream) {
+  hs::Kv4Rows a{};
+  hs_status r = check_rows(a, block_table, table_stride, table_width, num_pages, page_size,
+                           cu_seqlens, seq_lens, num_seqs, total_tokens);
+  if (r != HS_OK) return r;
+  if ((r = check_dtype(dtype)) != HS_OK) return r;
+  if ((r = check_width("dk", dk)) != HS_OK) return r;
+  if (dv != 0 && (r = check_width("dv", dv)) != HS_OK) return r;
+  if (!k || !k_cache) return fail(HS_ERR_INVALID_ARG, "k or k_cache is NULL");
+  if (dv == 0 ? (v || v_cache) : (!v || !v_cache))
+    return fail(HS_ERR_INVALID_ARG, "v and v_cache go with dv > 0, and only with it");
+  if (k_row_stride < dk)
+    return fail(HS_ERR_INVALID_ARG, "k_row_stride %lld < dk", (long long)k_row_stride);
+  if (v_row_stride < dv)
+    return fail(HS_ERR_INVALID_ARG, "v_row_stride %lld < dv", (long long)v_row_stride);
+  if (!aligned16(k_cache) || !aligned16(v_cache))
+    return fail(HS_ERR_INVALID_ARG, "a cache is not 16-byte aligned");
+  if (total_tokens == 0) return HS_OK;
+  r = status_ptr(&a.status);
+  if (r != HS_OK) return r;
+  const hs::Kv4Append w{k, k_row_stride, v, v_row_stride, k_cache, v_cache, dk, dv, dtype};
+  return launched_on(hs::launch_kv4_append(a, w, stream), "4-bit cache append", HS_PATH_SIMT);
+}
+
+hs_status hs_kv4_read(const void* cache, int width, const int32_t* block_table,
+                      int64_t table_stride, int table_width, int num_pages, int page_size,
+                      const int32_t* cu_seqlens, const int32_t* seq_lens, int num_seqs,
+                      int total_tokens, void* out, int64_t out_row_stride, hs_dtype dtype,
+                      hs_stream_t stream) {
+  hs::Kv4Rows a{};
+  hs_status r = check_rows(a, block_table, table_stride, table_width, num_pages, page_size,
+                           cu_seqlens, seq_lens, num_seqs, total_tokens);
+  if (r != HS_OK) return r;
+  if ((r = check_dtype(dtype)) != HS_OK) return r;
+  if ((r = check_width("width", width)) != HS_OK) return r;
+  if (!cache || !out) return fail(HS_ERR_INVALID_ARG, "cache or out is NULL");
+  if (out_row_stride < width)
+    return fail(HS_ERR_INVALID_ARG, "out_row_stride %lld < width", (long long)out_row_stride);
+  if (!aligned16(cache)) return fail(HS_ERR_INVALID_ARG, "the cache is not 16-byte aligned");
+  if (total_tokens == 0) return HS_OK;
+  r = status_ptr(&a.status);
+  if (r != HS_OK) return r;
+  return launched_on(hs::launch_kv4_read(a, cache, width, out, out_row_stride, dtype, stream),
+                     "4-bit cache read", HS_PATH_SIMT);
+}
+
+hs_status hs_kv4_mqa_decode(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            int64_t table_stride, int table_width, int num_pages, int page_size,
+                            const int32_t* seq_lens, int num_seqs, int max_seqlen, int num_heads,
+                            int dk, int dv, hs_dtype dtype, float softmax_scale, int window,
+                            int num_first, const float* sink, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, hs_stream_t stream) {
+  hs_status r =
+      check_pages(block_table, table_stride, table_width, num_pages, page_size, num_seqs);
+  if (r != HS_OK) return r;
+  if ((r = check_dtype(dtype)) != HS_OK) return r;
+  if ((r = check_width("dk", dk)) != HS_OK) return r;
+  if ((r = check_width("dv", dv)) != HS_OK) return r;
+  if (num_heads < 1 || num_heads > kMaxHeads)
+    return fail(HS_ERR_UNSUPPORTED, "num_heads %d not in [1, %d]", num_heads, kMaxHeads);
+  if ((int64_t)num_seqs * num_heads > INT32_MAX)
+    return fail(HS_ERR_UNSUPPORTED, "num_seqs * num_heads does not fit 31 bits");
+  if (num_seqs > 0 && max_seqlen < 1)
+    return fail(HS_ERR_INVALID_ARG, "max_seqlen must be >= 1");
+  if (!q || !k_cache || !seq_lens)
+    return fail(HS_ERR_INVALID_ARG, "q, k_cache or seq_lens is NULL");
+  if (!out || !lse) return fail(HS_ERR_INVALID_ARG, "out or lse is NULL");
+  if (!v_cache && dv > dk)
+    return fail(HS_ERR_INVALID_ARG, "without a v_cache dv %d must not exceed dk %d", dv, dk);
+  if (q_head_stride < dk)
+    return fail(HS_ERR_INVALID_ARG, "q_head_stride %lld < dk", (long long)q_head_stride);
+  if (q_row_stride < (int64_t)num_heads * q_head_stride)
+    return fail(HS_ERR_INVALID_ARG, "q_row_stride %lld < num_heads * q_head_stride",
+                (long long)q_row_stride);
+  if (!isfinite(softmax_scale)) return fail(HS_ERR_INVALID_ARG, "softmax_scale is not finite");
+  if (window < 0 || num_first < 0)
+    return fail(HS_ERR_INVALID_ARG, "window %d or num_first %d < 0", window, num_first);
+  if (window == 0 && num_first != 0)
+    return fail(HS_ERR_INVALID_ARG, "num_first without a window");
+  if (!aligned16(k_cache) || !aligned16(v_cache))
+    return fail(HS_ERR_INVALID_ARG, "a cache is not 16-byte aligned");
+  if (num_seqs == 0) return HS_OK;
+  const size_t need = hs_workspace_size(HS_OP_KV4_MQA_DECODE, num_seqs, num_seqs, max_seqlen,
+                                        num_heads, dk, dv, dtype, page_size);
+  if (!workspace || workspace_bytes < need)
+    return fail(HS_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
+                workspace ? workspace_bytes : (size_t)0);
+  if (!aligned16(workspace)) return fail(HS_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
+  hs::Kv4Decode a{};
+  a.q = q;
+  a.q_row_stride = q_row_stride;
+  a.q_head_stride = q_head_stride;
+  a.k_cache = static_cast<const uint8_t*>(k_cache);
+  a.v_cache = static_cast<const uint8_t*>(v_cache);
+  a.table = block_table;
+  a.table_stride = table_stride;
+  a.table_width = table_width;
+  a.num_pages = num_pages;
+  a.ps_log2 = log2_of(page_size);
+  a.seq_lens = seq_lens;
+  a.num_seqs = num_seqs;
+  a.max_seqlen = max_seqlen;
+  a.num_heads = num_heads;
+  a.dk = dk;
+  a.dv = dv;
+  a.dtype = dtype;
+  a.scale = softmax_scale > 0.f ? softmax_scale : 1.0f / sqrtf((float)dk);
+  a.window = window < max_seqlen ? window : max_seqlen;  // beyond every sequence: the same
+  a.first = num_first < max_seqlen ? num_first : max_seqlen;
+  a.sink = sink;
+  a.out = out;
+  a.lse = lse;
+  a.workspace = workspace;
+  r = status_ptr(&a.status);
+  if (r != HS_OK) return r;
+  return launched_on(hs::launch_simt_kv4_decode(a, stream), "simt 4-bit cache decode",
+                     HS_PATH_SIMT);
 }
 
 }  // extern "C"

@@ -42,6 +42,8 @@ struct AttnArgs {
   const float* sink;   // may be null
   void* out;
   float* lse;
+  int first = 0;       // swa only: first tokens of the document that stay visible
+  bool with_first = false;  // the call is hs_swa_first_mqa_fwd (first may be 0)
   // optional combining epilogue (the SWA layer): out = gate_own * result +
   // gate_prev * prev; prev [T, H, Dv] of dtype, may alias out; gates [T, H]
   // fp32 or null (= 1).  prev == null: plain output.
@@ -72,10 +74,12 @@ struct BwdArgs {
   const void* out;
   const float* lse;
   const void* dout;
-  float* dq;
-  float* dkey;
-  float* dval;
+  void* dq;            // fp32, or the inputs' type (grad_like_input)
+  void* dkey;
+  void* dval;
   float* dsink;        // may be null
+  int first = 0;       // swa only: first tokens of the document that stay visible
+  bool grad_like_input = false;  // dq, dkey, dval in p.dtype instead of fp32
   void* workspace;     // simt_backward_workspace() bytes
   void* dkdv_ws;       // the tensor-core dk / dv pass's partial sums, or null
 };
@@ -124,6 +128,52 @@ cudaError_t launch_tc_attention(const AttnArgs& a, bool sparse, long long wait_l
 bool tc_full_supported(int num_heads, int dk, int dv, int block_size);
 size_t tc_full_workspace(int total_tokens, int nbmax);
 cudaError_t launch_tc_full(const FullArgs& f, long long wait_limit, cudaStream_t s);
+
+// The 4-bit paged cache (kv4.cuh): packed rows and where they live.
+struct Kv4Rows {
+  const int32_t* table;  // [num_seqs, table_stride] pages of each sequence
+  int64_t table_stride;
+  int table_width;       // valid entries of a table row
+  int num_pages, ps_log2;
+  const int32_t* cu;     // [num_seqs + 1] packed rows of each sequence
+  const int32_t* seq_lens;  // [num_seqs] cached rows, these ones included
+  int num_seqs, total_tokens;
+  int* status;
+};
+struct Kv4Append {
+  const void* k;
+  int64_t k_row_stride;
+  const void* v;         // null with dv == 0
+  int64_t v_row_stride;
+  void* k_cache;
+  void* v_cache;         // null with dv == 0
+  int dk, dv;
+  hs_dtype dtype;
+};
+struct Kv4Decode {
+  const void* q;
+  int64_t q_row_stride, q_head_stride;
+  const uint8_t* k_cache;
+  const uint8_t* v_cache;  // null: values are the first dv columns of the k rows
+  const int32_t* table;
+  int64_t table_stride;
+  int table_width, num_pages, ps_log2;
+  const int32_t* seq_lens;
+  int num_seqs, max_seqlen, num_heads, dk, dv;
+  hs_dtype dtype;
+  float scale;
+  int window, first;       // window 0: every position
+  const float* sink;       // may be null
+  void* out;
+  float* lse;
+  void* workspace;
+  int* status;
+};
+cudaError_t launch_kv4_append(const Kv4Rows& a, const Kv4Append& w, cudaStream_t s);
+cudaError_t launch_kv4_read(const Kv4Rows& a, const void* cache, int width, void* out,
+                            int64_t out_row_stride, hs_dtype dtype, cudaStream_t s);
+size_t simt_kv4_decode_workspace(int num_seqs, int num_heads, int max_seqlen, int dv);
+cudaError_t launch_simt_kv4_decode(const Kv4Decode& a, cudaStream_t s);
 
 // Records msg as the calling thread's hs_last_error() and returns st.
 hs_status report_error(hs_status st, const char* msg);

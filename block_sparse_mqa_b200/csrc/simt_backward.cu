@@ -43,10 +43,12 @@ struct BwdParams {
   const void* out;
   const float* lse;
   const void* dout;
-  float* dq;
-  float* dkey;
-  float* dval;
+  void* dq;            // fp32, or the inputs' type (like_input)
+  void* dkey;
+  void* dval;
   float* dsink;
+  int first;           // window: first tokens of the document that stay visible
+  bool like_input;
   float* delta;       // workspace [T, H]
   float* dsink_part;  // workspace [T, H]
   int G, KT;          // heads per group, keys per dq tile
@@ -55,6 +57,15 @@ struct BwdParams {
 template <typename T>
 __device__ __forceinline__ float ld(const void* base, int64_t i) {
   return to_f32<T>(static_cast<const T*>(base)[i]);
+}
+
+// Gradient element i: fp32, or rounded once to the inputs' type.
+template <typename T>
+__device__ __forceinline__ void st(void* base, int64_t i, float x, bool like_input) {
+  if (like_input)
+    static_cast<T*>(base)[i] = from_f32<T>(x);
+  else
+    static_cast<float*>(base)[i] = x;
 }
 
 // Entry s of idx row `row` is a selected block when 0 <= b <= bq and b is
@@ -157,7 +168,9 @@ __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
       }
       __syncthreads();
     }
-    const int nseg = kSparse ? nblk : 1;
+    // the window's segments: the first tokens before it, then the window
+    const int wlo = kSparse ? 0 : max(bos, t - a.window + 1);
+    const int nseg = kSparse ? nblk : 2;
     for (int g0 = 0; g0 < H; g0 += G) {
       const int gn = min(G, H - g0);
       for (int e = tid; e < gn * dk; e += kThreads) {
@@ -180,8 +193,8 @@ __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
           lo = bos + blist[sg] * a.B;
           hi = min(min(lo + a.B, eos), t + 1);
         } else {
-          lo = max(bos, t - a.window + 1);
-          hi = t + 1;
+          lo = sg == 0 ? bos : wlo;
+          hi = sg == 0 ? bos + min(a.first, wlo - bos) : t + 1;
         }
         for (int j0 = lo; j0 < hi; j0 += KT) {
           const int n = min(KT, hi - j0);
@@ -225,7 +238,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
       }
       for (int e = tid; e < gn * dk; e += kThreads) {
         const int g = e / dk, d = e - g * dk;
-        a.dq[((int64_t)t * H + g0 + g) * dk + d] = dqs[e];
+        st<T>(a.dq, ((int64_t)t * H + g0 + g) * dk + d, dqs[e], a.like_input);
       }
       __syncthreads();
     }
@@ -284,7 +297,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
       }
       // candidate queries t (those whose key set can meet [s0, s1)), in
       // chunks of kThreads: thread i tests t = c0 + i
-      const int tend = kSparse ? eos : min(eos, s1 - 1 + a.window);
+      const int tend = kSparse || s0 - bos < a.first ? eos : min(eos, s1 - 1 + a.window);
       const int ba = kSparse ? (s0 - bos) / a.B : 0, bb = kSparse ? (s1 - 1 - bos) / a.B : 0;
       for (int c0 = s0; c0 < tend; c0 += kThreads) {
         const int t = c0 + tid;
@@ -302,7 +315,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
           } else {
             for (int jj = 0; jj < n; ++jj) {
               const int j = s0 + jj;
-              if (j <= t && j > t - a.window) mask |= 1u << jj;
+              if (j <= t && (j > t - a.window || j - bos < a.first)) mask |= 1u << jj;
             }
           }
         }
@@ -379,11 +392,11 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
       }
       for (int e = tid; e < n * dk; e += kThreads) {
         const int jj = e / dk, d = e - jj * dk;
-        a.dkey[(int64_t)(s0 + jj) * dk + d] = dks[e];
+        st<T>(a.dkey, (int64_t)(s0 + jj) * dk + d, dks[e], a.like_input);
       }
       for (int e = tid; e < n * dv; e += kThreads) {
         const int jj = e / dv, d = e - jj * dv;
-        a.dval[(int64_t)(s0 + jj) * dv + d] = dvs[e];
+        st<T>(a.dval, (int64_t)(s0 + jj) * dv + d, dvs[e], a.like_input);
       }
       __syncthreads();
       s0 = s1;
@@ -465,11 +478,13 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
   a.dkey = b.dkey;
   a.dval = b.dval;
   a.dsink = b.dsink;
+  a.first = b.first;
+  a.like_input = b.grad_like_input;
   a.delta = static_cast<float*>(b.workspace);
   a.dsink_part = a.delta + (size_t)b.p.total_tokens * b.p.num_heads;
   if (b.p.dtype == HS_BF16) {
     // tensor cores: dq and dk / dv on tcgen05 (else every pass on CUDA cores)
-    const bool mma = allow_mma && tc_bwd_dq_supported(b.p) && tc_bwd_dkdv_supported(b.p) &&
+    const bool mma = allow_mma && b.first == 0 && !b.grad_like_input && tc_bwd_dq_supported(b.p) && tc_bwd_dkdv_supported(b.p) &&
                      (reinterpret_cast<uintptr_t>(b.dout) & 15) == 0 && b.dkdv_ws != nullptr;
     if (path) *path = mma ? HS_PATH_MMA : HS_PATH_SIMT;
     cudaError_t e = sparse ? launch_typed<__nv_bfloat16, true>(a, !mma, s)

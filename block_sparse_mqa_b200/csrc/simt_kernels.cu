@@ -166,12 +166,15 @@ simt_attention_kernel(AttnArgs a) {
   for (int r = 0; r < kMaxDvPerThread; ++r) acc[r] = 0.f;
   float m = -INFINITY, l = 0.f;
 
-  int nseg, wlo = 0;
+  // nfirst: segments of the document's first tokens that lie before the window
+  int nseg, wlo = 0, fhi = 0, nfirst = 0;
   if (kSparse) {
     nseg = a.topk;
   } else {
     wlo = max(bos, t - a.window + 1);
-    nseg = (t + 1 - wlo + 127) / 128;
+    fhi = bos + min(a.first, wlo - bos);
+    nfirst = (fhi - bos + 127) / 128;
+    nseg = nfirst + (t + 1 - wlo + 127) / 128;
   }
   const int bq = (t - bos) / a.block_size;
   for (int sgi = 0; sgi < nseg; ++sgi) {
@@ -187,8 +190,11 @@ simt_attention_kernel(AttnArgs a) {
       }
       lo = bos + b * a.block_size;
       hi = min(lo + a.block_size, t + 1);
+    } else if (sgi < nfirst) {
+      lo = bos + sgi * 128;
+      hi = min(lo + 128, fhi);
     } else {
-      lo = wlo + sgi * 128;
+      lo = wlo + (sgi - nfirst) * 128;
       hi = min(lo + 128, t + 1);
     }
     const int cnt = hi - lo;

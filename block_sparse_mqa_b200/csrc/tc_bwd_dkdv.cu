@@ -645,8 +645,8 @@ cudaError_t launch_tc_bwd_dkdv(const BwdArgs& b, bool sparse, const float* delta
   a.scale_log2 = p.scale * kLog2e;
   a.lse = b.lse;
   a.delta = delta;
-  a.dkey = b.dkey;
-  a.dval = b.dval;
+  a.dkey = static_cast<float*>(b.dkey);
+  a.dval = static_cast<float*>(b.dval);
   a.status = p.status;
   a.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
   range_split(p.total_tokens, a.rlen, a.nrange);

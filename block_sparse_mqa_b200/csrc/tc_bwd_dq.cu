@@ -615,7 +615,7 @@ cudaError_t launch_tc_bwd_dq(const BwdArgs& b, bool sparse, const float* delta,
   a.scale_log2 = p.scale * kLog2e;
   a.lse = b.lse;
   a.delta = delta;
-  a.dq = b.dq;
+  a.dq = static_cast<float*>(b.dq);
   a.status = p.status;
   a.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
   auto kern = sparse ? tc_bwd_dq_kernel<true> : tc_bwd_dq_kernel<false>;

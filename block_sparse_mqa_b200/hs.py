@@ -39,6 +39,9 @@ HS_OP_SPARSE_MQA_BWD = 4
 HS_OP_SWA_MQA_BWD = 5
 HS_OP_BLOCK_SCORE_ATTN = 6
 HS_OP_SWA_LAYER = 7
+HS_OP_SWA_FIRST_MQA = 8
+HS_OP_SWA_FIRST_MQA_BWD = 9
+HS_OP_KV4_MQA_DECODE = 10
 
 HS_PATH_SIMT = 0
 HS_PATH_TCGEN05 = 1
@@ -51,6 +54,8 @@ EXPORTS = (
     "hs_selftest_wait", "hs_status_string", "hs_last_error", "hs_version",
     "hs_block_score_static", "hs_sparse_mqa_bwd", "hs_swa_mqa_bwd",
     "hs_block_score_attn_fwd", "hs_swa_layer_fwd", "hs_last_path",
+    "hs_swa_first_mqa_fwd", "hs_swa_first_mqa_bwd", "hs_kv4_page_bytes", "hs_kv4_append",
+    "hs_kv4_read", "hs_kv4_mqa_decode",
 )
 
 
@@ -99,6 +104,21 @@ def lib() -> ctypes.CDLL:
     L.hs_swa_layer_fwd.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64,
                                    _vp, _int, _int, _int, _int, _int, _int, _int, _flt, _int,
                                    _vp, _vp, _int, _int, _vp, _vp, _vp, _vp, _vp, _vp, _vp]
+    L.hs_swa_first_mqa_fwd.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _int, _int,
+                                       _int, _int, _int, _int, _int, _flt, _int, _int, _vp, _vp,
+                                       _vp, _vp]
+    L.hs_swa_first_mqa_bwd.argtypes = [_vp, _i64, _i64, _vp, _i64, _vp, _i64, _vp, _int, _int,
+                                       _int, _int, _int, _int, _int, _flt, _int, _int, _vp, _vp,
+                                       _vp, _vp, _vp, _vp, _vp, _vp, _vp, _szt, _vp]
+    pages = [_vp, _i64, _int, _int, _int]  # table, stride, width, num_pages, page_size
+    L.hs_kv4_page_bytes.argtypes = [_int, _int]
+    L.hs_kv4_page_bytes.restype = _szt
+    L.hs_kv4_append.argtypes = [_vp, _i64, _vp, _i64, _vp, _vp, *pages, _vp, _vp, _int, _int,
+                                _int, _int, _int, _vp]
+    L.hs_kv4_read.argtypes = [_vp, _int, *pages, _vp, _vp, _int, _int, _vp, _i64, _int, _vp]
+    L.hs_kv4_mqa_decode.argtypes = [_vp, _i64, _i64, _vp, _vp, *pages, _vp, _int, _int, _int,
+                                    _int, _int, _int, _flt, _int, _int, _vp, _vp, _vp, _vp, _szt,
+                                    _vp]
     L.hs_workspace_size.argtypes = [_int] * 9
     L.hs_workspace_size.restype = _szt
     L.hs_path.argtypes = [_int] * 6
@@ -115,7 +135,9 @@ def lib() -> ctypes.CDLL:
     L.hs_last_path.restype = _int
     for fn in ("hs_block_score", "hs_select_topk", "hs_sparse_mqa_fwd", "hs_swa_mqa_fwd",
                "hs_poll_status", "hs_block_score_static", "hs_sparse_mqa_bwd",
-               "hs_swa_mqa_bwd", "hs_block_score_attn_fwd", "hs_swa_layer_fwd"):
+               "hs_swa_mqa_bwd", "hs_block_score_attn_fwd", "hs_swa_layer_fwd",
+               "hs_swa_first_mqa_fwd", "hs_swa_first_mqa_bwd", "hs_kv4_append", "hs_kv4_read",
+               "hs_kv4_mqa_decode"):
         getattr(L, fn).restype = _int
     _lib = L
     return L
@@ -451,6 +473,242 @@ def hs_swa_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, out, lse, 
         _ptr(g[0]), _ptr(g[1]), _ptr(g[2]), _ptr(g[3]), _ptr(ws),
         0 if ws is None else ws.numel(), _stream(q.device)))
     return g
+
+
+def _same_device(*ts):
+    _need_cuda(*ts)
+    if len({t.device for t in ts if t is not None}) > 1:
+        raise ValueError("all tensors must be on one device")
+
+
+def _int32(name, t, dims=1):
+    if t.dtype != torch.int32 or t.dim() != dims or t.stride(-1) != 1:
+        raise ValueError("%s must be int32 with %d dimension%s, the last one contiguous"
+                         % (name, dims, "s" * (dims > 1)))
+
+
+def _rows(name, t, n, like=None):
+    if t.dim() != 2 or t.stride(1) != 1 or (n is not None and t.shape[0] != n):
+        raise ValueError("%s must be [%s, width] with contiguous rows" % (name, n or "T"))
+    if like is not None and t.dtype != like.dtype:
+        raise ValueError("%s must have the other tensors' dtype %s" % (name, like.dtype))
+
+
+def _row_stride(t):
+    """Row stride of [T, width] rows (that of a single row may be anything)."""
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])
+
+
+def _q_strides(q):
+    """Row and head stride of q [T, H, Dk] (those of a single row or head may be anything)."""
+    if q.dim() != 3 or q.stride(2) != 1:
+        raise ValueError("q must be [T, H, Dk] with a contiguous last dimension")
+    T, H, Dk = q.shape
+    qhs = q.stride(1) if H > 1 else max(q.stride(1), Dk)
+    return (q.stride(0) if T > 1 else max(q.stride(0), H * qhs)), qhs
+
+
+def _out(name, t, shape, dtype):
+    if tuple(t.shape) != tuple(shape) or t.dtype != dtype or not t.is_contiguous():
+        raise ValueError("%s must be contiguous %s %s" % (name, dtype, list(shape)))
+
+
+def _sink_ok(sink, H):
+    if sink is not None:
+        _out("sink", sink, (H,), torch.float32)
+
+
+def _swa_first_check(q, k, v, cu_seqlens, sink, *more):
+    _same_device(q, k, v, cu_seqlens, sink, *more)
+    if q.dim() != 3:
+        raise ValueError("q must be [T, H, Dk]")
+    T, H, Dk = q.shape
+    _rows("k", k, T, q)
+    _rows("v", v, T, q)
+    if k.shape[1] != Dk:
+        raise ValueError("k must be [T, Dk]")
+    _int32("cu_seqlens", cu_seqlens)
+    _sink_ok(sink, H)
+    return T, H, Dk, v.shape[1]
+
+
+def hs_swa_first_mqa_fwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_first: int,
+                         sink=None, softmax_scale: float = 0.0, out=None, lse=None):
+    """Step 4 with the first num_first tokens of each document always visible.
+    Returns (out [T,H,Dv] in q's dtype, lse [T,H] f32)."""
+    T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse)
+    qrs, qhs = _q_strides(q)
+    o, l = _attn_out(q, v, out, lse)
+    _out("out", o, (T, H, Dv), q.dtype)
+    _out("lse", l, (T, H), torch.float32)
+    if T == 0:
+        return o, l
+    with torch.cuda.device(q.device):
+        _check(lib().hs_swa_first_mqa_fwd(
+            _ptr(q), qrs, qhs, _ptr(k), _row_stride(k), _ptr(v), _row_stride(v),
+            _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen), H, Dk, Dv,
+            _dtype_code(q), float(softmax_scale), int(window), int(num_first), _ptr(sink),
+            _ptr(o), _ptr(l),
+            _stream(q.device)))
+    return o, l
+
+
+def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_first: int, out,
+                         lse, dout, sink=None, softmax_scale: float = 0.0, grads=None,
+                         workspace=None):
+    """Backward of hs_swa_first_mqa_fwd.  Returns (dq [T,H,Dk], dk [T,Dk], dv [T,Dv])
+    in q's dtype and dsink [H] float32 (None without a sink)."""
+    T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse, dout, workspace,
+                                    *(grads or ()))
+    qrs, qhs = _q_strides(q)
+    _out("out", out, (T, H, Dv), q.dtype)
+    _out("dout", dout, (T, H, Dv), q.dtype)
+    _out("lse", lse, (T, H), torch.float32)
+    if grads is None:
+        new = lambda *shape: torch.empty(shape, device=q.device, dtype=q.dtype)
+        grads = (new(T, H, Dk), new(T, Dk), new(T, Dv),
+                 torch.empty((H,), device=q.device) if sink is not None else None)
+    for name, g, shape in zip(("dq", "dk", "dv"), grads, ((T, H, Dk), (T, Dk), (T, Dv))):
+        _out(name, g, shape, q.dtype)
+    _sink_ok(grads[3], H)
+    nd = cu_seqlens.numel() - 1
+    if T == 0:
+        if grads[3] is not None:
+            grads[3].zero_()
+        return grads
+    if workspace is None:
+        workspace = torch.empty(workspace_size(HS_OP_SWA_FIRST_MQA_BWD, T, nd, max_seqlen, H, Dk,
+                                               Dv, q.dtype, 64),
+                                device=q.device, dtype=torch.uint8)
+    with torch.cuda.device(q.device):
+        _check(lib().hs_swa_first_mqa_bwd(
+            _ptr(q), qrs, qhs, _ptr(k), _row_stride(k), _ptr(v), _row_stride(v),
+            _ptr(cu_seqlens), nd, T, int(max_seqlen), H, Dk, Dv, _dtype_code(q),
+            float(softmax_scale), int(window), int(num_first), _ptr(sink), _ptr(out), _ptr(lse), _ptr(dout), _ptr(grads[0]),
+            _ptr(grads[1]), _ptr(grads[2]), _ptr(grads[3]), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(q.device)))
+    return grads
+
+
+def kv4_page_bytes(width: int, page_size: int) -> int:
+    """Bytes of one page of a 4-bit cache plane (ValueError if unsupported)."""
+    n = int(lib().hs_kv4_page_bytes(int(width), int(page_size)))
+    if n == 0:
+        raise ValueError("width must be a multiple of 32 up to 1024 and page_size 16, 32, 64 "
+                         "or 128, got %d and %d" % (width, page_size))
+    return n
+
+
+def kv4_cache(num_pages: int, width: int, page_size: int, device="cuda"):
+    """An empty cache plane: uint8 [num_pages, page bytes], zeroed."""
+    return torch.zeros((num_pages, kv4_page_bytes(width, page_size)), dtype=torch.uint8,
+                       device=device)
+
+
+def _plane(name, cache, width, page_size, like=None):
+    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.dim() != 2 or \
+            cache.shape[1] != kv4_page_bytes(width, page_size):
+        raise ValueError("%s must be contiguous uint8 [num_pages, %d] (width %d, page size %d)"
+                         % (name, kv4_page_bytes(width, page_size), width, page_size))
+    if like is not None and cache.shape[0] != like.shape[0]:
+        raise ValueError("k_cache and v_cache must have the same number of pages")
+
+
+def _table_args(block_table, seq_lens, num_pages, page_size):
+    _int32("block_table", block_table, 2)
+    _int32("seq_lens", seq_lens)
+    if block_table.shape[0] != seq_lens.numel():
+        raise ValueError("block_table must have one row per sequence")
+    # a single row's stride may be anything; the library wants at least the width
+    stride = max(block_table.stride(0), block_table.shape[1])
+    return _ptr(block_table), stride, block_table.shape[1], num_pages, int(page_size)
+
+
+def hs_kv4_append(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens, page_size: int):
+    """Quantise the packed rows k [T,Dk] (and v [T,Dv], or None with v_cache None)
+    to 4 bits and write them behind the rows their sequences already have;
+    seq_lens counts the new rows too (see include/hs.h)."""
+    _same_device(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens)
+    if (v is None) != (v_cache is None):
+        raise ValueError("v and v_cache go together")
+    _rows("k", k, None)
+    T = k.shape[0]
+    _plane("k_cache", k_cache, k.shape[1], page_size)
+    if v is not None:
+        _rows("v", v, T, k)
+        _plane("v_cache", v_cache, v.shape[1], page_size, k_cache)
+    _int32("cu_seqlens", cu_seqlens)
+    if cu_seqlens.numel() != seq_lens.numel() + 1:
+        raise ValueError("cu_seqlens must have one entry more than seq_lens")
+    table = _table_args(block_table, seq_lens, k_cache.shape[0], page_size)
+    if T == 0:
+        return
+    with torch.cuda.device(k.device):
+        _check(lib().hs_kv4_append(
+            _ptr(k), _row_stride(k), _ptr(v), 0 if v is None else _row_stride(v), _ptr(k_cache),
+            _ptr(v_cache), *table, _ptr(cu_seqlens), _ptr(seq_lens), seq_lens.numel(), T,
+            k.shape[1], 0 if v is None else v.shape[1], _dtype_code(k), _stream(k.device)))
+
+
+def hs_kv4_read(cache, width: int, block_table, cu_seqlens, seq_lens, page_size: int,
+                total_tokens: int, out=None, dtype=torch.bfloat16):
+    """The values of the last rows of each sequence (as many as cu_seqlens has for
+    it), packed: [total_tokens, width].  Rows behind the last sequence are left
+    as they are (unset in a new tensor)."""
+    _same_device(cache, block_table, cu_seqlens, seq_lens, out)
+    _plane("cache", cache, width, page_size)
+    _int32("cu_seqlens", cu_seqlens)
+    if cu_seqlens.numel() != seq_lens.numel() + 1:
+        raise ValueError("cu_seqlens must have one entry more than seq_lens")
+    table = _table_args(block_table, seq_lens, cache.shape[0], page_size)
+    o = out if out is not None else torch.empty((total_tokens, width), device=cache.device,
+                                                dtype=dtype)
+    _rows("out", o, total_tokens)
+    if o.shape[1] != width:
+        raise ValueError("out must be [total_tokens, width]")
+    if total_tokens == 0:
+        return o
+    with torch.cuda.device(cache.device):
+        _check(lib().hs_kv4_read(
+            _ptr(cache), int(width), *table, _ptr(cu_seqlens), _ptr(seq_lens), seq_lens.numel(),
+            int(total_tokens), _ptr(o), _row_stride(o), _dtype_code(o), _stream(cache.device)))
+    return o
+
+
+def hs_kv4_mqa_decode(q, k_cache, v_cache, block_table, seq_lens, max_seqlen: int, page_size: int,
+                      dv: int, window: int = 0, num_first: int = 0, sink=None,
+                      softmax_scale: float = 0.0, out=None, lse=None, workspace=None):
+    """One query token per sequence over the 4-bit cache (v_cache None: values are
+    the first dv columns of the keys); window 0 attends everything, else the
+    first num_first tokens and the last `window`.  Returns (out [S,H,dv] in
+    q's dtype, lse [S,H] f32)."""
+    _same_device(q, k_cache, v_cache, block_table, seq_lens, sink, out, lse, workspace)
+    qrs, qhs = _q_strides(q)
+    S, H, Dk = q.shape
+    if seq_lens.numel() != S:
+        raise ValueError("q must have one row per sequence")
+    _plane("k_cache", k_cache, Dk, page_size)
+    if v_cache is not None:
+        _plane("v_cache", v_cache, dv, page_size, k_cache)
+    table = _table_args(block_table, seq_lens, k_cache.shape[0], page_size)
+    _sink_ok(sink, H)
+    o = out if out is not None else torch.empty((S, H, dv), device=q.device, dtype=q.dtype)
+    l = lse if lse is not None else torch.empty((S, H), device=q.device, dtype=torch.float32)
+    _out("out", o, (S, H, dv), q.dtype)
+    _out("lse", l, (S, H), torch.float32)
+    if S == 0:
+        return o, l
+    if workspace is None:
+        workspace = torch.empty(workspace_size(HS_OP_KV4_MQA_DECODE, S, S, max_seqlen, H, Dk, dv,
+                                               q.dtype, page_size),
+                                device=q.device, dtype=torch.uint8)
+    with torch.cuda.device(q.device):
+        _check(lib().hs_kv4_mqa_decode(
+            _ptr(q), qrs, qhs, _ptr(k_cache), _ptr(v_cache), *table, _ptr(seq_lens), S,
+            int(max_seqlen), H, Dk, int(dv), _dtype_code(q), float(softmax_scale), int(window),
+            int(num_first), _ptr(sink), _ptr(o), _ptr(l), _ptr(workspace),
+            workspace.numel() * workspace.element_size(), _stream(q.device)))
+    return o, l
 
 
 def hs_forward(q, k, v, cu_seqlens, max_seqlen: int, block_size: int, topk: int, window: int,

@@ -24,6 +24,14 @@
  * is the SWA layer: its window attention plus a block-sparse branch over the
  * full layer's shared KV, combined.
  *
+ * For models that run on past their window, and for serving them:
+ *   hs_swa_first_mqa_fwd / _bwd  step 4's attention whose first tokens of
+ *                      each document stay visible, and its backward
+ *   hs_kv4_append / hs_kv4_read  rows into a paged cache of 4-bit keys and
+ *                      values, and back
+ *   hs_kv4_mqa_decode  one query token per sequence over that cache, over
+ *                      all of it or over first tokens and window
+ *
  * Conventions shared by every call
  * --------------------------------
  * Pointers named q, k, v, out, lse, block_score, block_lse, idx, sink and
@@ -102,7 +110,10 @@ typedef enum hs_op {
   HS_OP_SPARSE_MQA_BWD = 4,
   HS_OP_SWA_MQA_BWD = 5,
   HS_OP_BLOCK_SCORE_ATTN = 6,
-  HS_OP_SWA_LAYER = 7
+  HS_OP_SWA_LAYER = 7,
+  HS_OP_SWA_FIRST_MQA = 8,
+  HS_OP_SWA_FIRST_MQA_BWD = 9,
+  HS_OP_KV4_MQA_DECODE = 10 /* hs_workspace_size: total_tokens = num_seqs */
 } hs_op;
 
 /* Kernel family a call will use, as returned by hs_path(). */
@@ -387,6 +398,147 @@ hs_status hs_swa_layer_fwd(const void* q, int64_t q_row_stride, int64_t q_head_s
                            float* lse_sparse, hs_stream_t stream);
 
 /*
+ * Sliding-window attention whose first tokens stay visible.
+ * No counterpart on the pages: it is step 4 for streams longer than the
+ * window, where the first few tokens of a document keep taking probability
+ * mass and dropping them disturbs every later token.
+ *
+ * Keys of query t in document [bos, eos): the window of hs_swa_mqa_fwd and
+ * the document's first num_first tokens, each key once and none after t:
+ *   S_t = { j <= t : j >= max(bos, t - window + 1)  or  bos <= j < bos + num_first }
+ * lse, out and the sink logit are defined as in hs_swa_mqa_fwd.  window >= 1;
+ * num_first >= 0 (0 = the window alone).  Values larger than a document mean
+ * all of it.  Keys and values outside S_t never reach a result: NaN and
+ * infinities in other documents, behind the query or between the first
+ * tokens and the window do no harm.  The arguments are hs_swa_mqa_fwd's.
+ */
+hs_status hs_swa_first_mqa_fwd(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                               const void* k, int64_t k_row_stride,
+                               const void* v, int64_t v_row_stride,
+                               const int32_t* cu_seqlens, int num_docs, int total_tokens,
+                               int max_seqlen, int num_heads, int dk, int dv, hs_dtype dtype,
+                               float softmax_scale, int window, int num_first,
+                               const float* sink, void* out, float* lse, hs_stream_t stream);
+
+/*
+ * Backward of hs_swa_first_mqa_fwd: the formulas and arguments of
+ * hs_swa_mqa_bwd over the key sets S_t above.  A first token collects
+ * gradients from every later query of its document.
+ * dq [T, H, Dk], dkey [T, Dk] and dval [T, Dv] are of `dtype`, the type of
+ * the tensors they belong to (step 4's backward returns fp32): sums run in
+ * fp32 and are rounded once.  dsink [H] is fp32.  Results are deterministic.
+ * Workspace: hs_workspace_size(HS_OP_SWA_FIRST_MQA_BWD, ...), the size and
+ * rules of hs_sparse_mqa_bwd.
+ * A query whose own q, dout, out or lse row holds NaN or an infinity spoils
+ * the gradients of the keys it attends, and may spoil those of the up to 31
+ * neighbours of such a key in the same document.
+ */
+hs_status hs_swa_first_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                               const void* k, int64_t k_row_stride,
+                               const void* v, int64_t v_row_stride,
+                               const int32_t* cu_seqlens, int num_docs, int total_tokens,
+                               int max_seqlen, int num_heads, int dk, int dv, hs_dtype dtype,
+                               float softmax_scale, int window, int num_first,
+                               const float* sink, const void* out, const float* lse,
+                               const void* dout, void* dq, void* dkey, void* dval, float* dsink,
+                               void* workspace, size_t workspace_bytes, hs_stream_t stream);
+
+/* ------------------------------------------------- 4-bit paged KV cache
+ *
+ * For serving (no counterpart on the pages).  A cache plane holds rows of
+ * `width` elements (a multiple of 32 up to 1024: Dk for keys, Dv for values)
+ * in num_pages pages of page_size rows (16, 32, 64 or 128), 4.25 bits an
+ * element when width is a multiple of 128:
+ *   groups of 32 elements share a scale, an unsigned 8-bit float with 5
+ *   exponent and 3 mantissa bits (the bits 7..14 of an fp16 number); a code
+ *   n in 0..15 stands for (n - 8) * scale, which is exact in bf16 and fp32.
+ * Page layout: codes [width / 32][page_size][16 bytes], then scales
+ * [ceil(width / 128)][page_size][4 bytes]; hs_kv4_page_bytes() gives its
+ * size.  Inside a group's four little-endian 32-bit words, word w holds
+ * elements 8w + 2k in bits 4k..4k+3 and 8w + 2k + 1 in bits 16+4k..19+4k.
+ * In the absorbed-MLA layout the values are the first Dv columns of the key
+ * rows: keep one plane and pass v_cache = NULL to the decode.
+ *
+ *   cache        num_pages * hs_kv4_page_bytes(width, page_size) bytes,
+ *                16-byte aligned.
+ *   block_table  [num_seqs, table_stride] int32, the first table_width
+ *                entries of a row valid: entry i is the page that holds the
+ *                sequence's rows i * page_size ...  Only entries that a row
+ *                or key needs are read; one outside [0, num_pages), or a row
+ *                past table_width, is HS_ERR_INVALID_INDEX in the device
+ *                status: a write is skipped, a read row is left as it was,
+ *                and a decoded sequence's output is then unspecified.
+ *                Sequences may share pages they only read.  Two rows of one
+ *                call must not go to the same place.
+ *   seq_lens     [num_seqs] int32 device: rows of each sequence in the
+ *                cache, those of this call included.
+ *   cu_seqlens   [num_seqs + 1] int32 device: row i of the packed tensor of
+ *                sequence s (cu_seqlens[s] <= i < cu_seqlens[s+1]) is cached
+ *                row seq_lens[s] - (cu_seqlens[s+1] - i): the call handles
+ *                the LAST rows of each sequence (all of them when
+ *                cu_seqlens' steps are seq_lens).  Sequences may have no rows.
+ *                Packed rows from cu_seqlens[num_seqs] to total_tokens are
+ *                padding: not read and not written.
+ * Calls are asynchronous on `stream`; the caller orders an append before the
+ * reads that need it.
+ */
+
+/* Bytes of one page, 0 for a width or page size that is not supported. */
+size_t hs_kv4_page_bytes(int width, int page_size);
+
+/*
+ * Quantises the rows k [T, Dk] (and v [T, Dv], of one dtype) and writes them
+ * to the cache.  Per group of 32: scale = the smallest representable one
+ * with 7 * scale >= max |x|, code = 8 + rint(x / scale) (ties to even).  A
+ * group that holds NaN or an infinity reads back as NaN; |x| above 430080
+ * saturates; the smallest scale is 2^-17.
+ * dv = 0 with v = v_cache = NULL writes keys only.
+ */
+hs_status hs_kv4_append(const void* k, int64_t k_row_stride, const void* v, int64_t v_row_stride,
+                        void* k_cache, void* v_cache, const int32_t* block_table,
+                        int64_t table_stride, int table_width, int num_pages, int page_size,
+                        const int32_t* cu_seqlens, const int32_t* seq_lens, int num_seqs,
+                        int total_tokens, int dk, int dv, hs_dtype dtype, hs_stream_t stream);
+
+/* The values of cached rows as out [T, width] of `dtype` (exact in both). */
+hs_status hs_kv4_read(const void* cache, int width, const int32_t* block_table,
+                      int64_t table_stride, int table_width, int num_pages, int page_size,
+                      const int32_t* cu_seqlens, const int32_t* seq_lens, int num_seqs,
+                      int total_tokens, void* out, int64_t out_row_stride, hs_dtype dtype,
+                      hs_stream_t stream);
+
+/*
+ * Single-token MQA attention over the cache: the query of sequence s sits at
+ * its last cached position, len = seq_lens[s] (its own key is in the cache).
+ * Attended positions: all of [0, len) when window = 0 (num_first must be 0
+ * then), else [0, num_first) and [len - window, len) clipped to [0, len),
+ * which is hs_swa_first_mqa_fwd's set for t = len - 1.  Pages of other
+ * positions are not read and need not exist.  lse, out and the sink logit
+ * are hs_swa_mqa_fwd's.  A sequence of length 0 gives out = 0 and lse =
+ * sink (-inf without one).
+ *
+ *   q           [num_seqs, H, Dk] of `dtype`
+ *   k_cache     plane of width Dk; v_cache plane of width Dv with the same
+ *               block table, or NULL: the first Dv <= Dk columns of the keys
+ *   max_seqlen  host-side bound of seq_lens (a longer one is
+ *               HS_ERR_INVALID_ARG in the device status, and is treated as 0)
+ *   out         [num_seqs, H, Dv] of `dtype`, contiguous; lse [num_seqs, H] fp32
+ *   workspace   hs_workspace_size(HS_OP_KV4_MQA_DECODE, num_seqs, num_seqs,
+ *               max_seqlen, H, Dk, Dv, dtype, page_size) bytes, 16-byte
+ *               aligned, contents on entry do not matter; calls that may
+ *               overlap must not share one.
+ * Results are deterministic; how a sequence's keys are split over the GPU,
+ * and so the last bits, depends on the whole batch's lengths.
+ */
+hs_status hs_kv4_mqa_decode(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* k_cache, const void* v_cache, const int32_t* block_table,
+                            int64_t table_stride, int table_width, int num_pages, int page_size,
+                            const int32_t* seq_lens, int num_seqs, int max_seqlen, int num_heads,
+                            int dk, int dv, hs_dtype dtype, float softmax_scale, int window,
+                            int num_first, const float* sink, void* out, float* lse,
+                            void* workspace, size_t workspace_bytes, hs_stream_t stream);
+
+/*
  * Step 1 for callers that cannot allocate device memory.
  * The method has no counterpart of this call; it is a deployment aid.
  *
@@ -431,8 +583,8 @@ hs_status hs_block_score_static(const void* q, int64_t q_row_stride, int64_t q_h
 /* ---------------------------------------------------------------- helpers */
 
 /* Bytes of `workspace` that op needs for these sizes (0 = none).
- * HS_OP_BLOCK_SCORE, HS_OP_BLOCK_SCORE_ATTN and the two backward ops use a
- * workspace. */
+ * HS_OP_BLOCK_SCORE, HS_OP_BLOCK_SCORE_ATTN, the backward ops and
+ * HS_OP_KV4_MQA_DECODE use a workspace. */
 size_t hs_workspace_size(int op, int total_tokens, int num_docs, int max_seqlen,
                          int num_heads, int dk, int dv, hs_dtype dtype, int block_size);
 

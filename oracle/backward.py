@@ -43,9 +43,11 @@ from typing import Optional
 
 import numpy as np
 
-from .hysparse import (_f64, _scale, doc_bounds, sparse_key_set, window_key_set)
+from .hysparse import (_f64, _scale, doc_bounds, first_window_key_set, sparse_key_set,
+                       window_key_set)
 
-__all__ = ["attend_bwd", "sparse_mqa_bwd", "swa_mqa_bwd", "dense_causal_bwd"]
+__all__ = ["attend_bwd", "sparse_mqa_bwd", "swa_mqa_bwd", "swa_first_mqa_bwd",
+           "dense_causal_bwd"]
 
 
 def attend_bwd(q_t, keys, k, v, sink, scale: float, dout_t):
@@ -125,6 +127,15 @@ def swa_mqa_bwd(q, k, v, dout, cu_seqlens, window: int, sink=None, scale=None):
 
     def keys(t, bos, eos):
         return window_key_set(t, bos, window)
+
+    return _bwd(q, k, v, dout, cu_seqlens, sink, scale, keys)
+
+
+def swa_first_mqa_bwd(q, k, v, dout, cu_seqlens, window: int, first: int, sink=None, scale=None):
+    """Backward of the window MQA forward with visible first tokens."""
+
+    def keys(t, bos, eos):
+        return first_window_key_set(t, bos, window, first)
 
     return _bwd(q, k, v, dout, cu_seqlens, sink, scale, keys)
 

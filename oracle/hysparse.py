@@ -262,6 +262,15 @@ def window_key_set(t: int, bos: int, window: int):
     return np.arange(lo, t + 1, dtype=np.int64)
 
 
+def first_window_key_set(t: int, bos: int, window: int, first: int):
+    """The window's keys and the document's first ``first`` tokens, each key
+    once, none after t (no counterpart on the pages: the window of step 4 for
+    streams longer than it)."""
+    lo = max(bos, t - int(window) + 1)
+    return np.concatenate((np.arange(bos, min(bos + int(first), lo), dtype=np.int64),
+                           np.arange(lo, t + 1, dtype=np.int64)))
+
+
 # ---------------------------------------------------------------------------
 # softmax attention with a sink
 # ---------------------------------------------------------------------------
@@ -339,6 +348,16 @@ def swa_mqa_fwd(q, k, v, cu_seqlens, window: int, sink=None, scale=None,
 
     def keys(i, t, bos, eos):
         return window_key_set(t, bos, window)
+
+    return _attend_rows(q, k, v, cu_seqlens, sink, scale, rows, keys)
+
+
+def swa_first_mqa_fwd(q, k, v, cu_seqlens, window: int, first: int, sink=None, scale=None,
+                      rows=None):
+    """Sliding-window MQA whose first tokens of each document stay visible."""
+
+    def keys(i, t, bos, eos):
+        return first_window_key_set(t, bos, window, first)
 
     return _attend_rows(q, k, v, cu_seqlens, sink, scale, rows, keys)
 

@@ -1,0 +1,109 @@
+"""Host checks of the window attention with visible first tokens and of the
+4-bit cache: refused before any CUDA call, so no GPU is needed."""
+
+import ctypes
+
+import pytest
+import torch
+
+from block_sparse_mqa_b200 import hs
+
+INV, UNS, WSP = hs.HS_ERR_INVALID_ARG, hs.HS_ERR_UNSUPPORTED, hs.HS_ERR_WORKSPACE
+
+
+def _call(fn, spec, kw):
+    a = dict(spec)
+    assert set(kw) <= set(a), kw
+    a.update(kw)
+    ptr = lambda x: ctypes.c_void_p(x) if x is not None else None
+    types = getattr(hs.lib(), fn).argtypes
+    st = getattr(hs.lib(), fn)(*[ptr(v) if t is ctypes.c_void_p else v for v, t in zip(a.values(), types)])
+    assert st == hs.HS_OK or hs.lib().hs_last_error()
+    return st
+
+
+ATT = dict(q=256, qrs=64 * 576, qhs=576, k=256, krs=576, v=256, vrs=512, cu=256, nd=1, T=100, maxlen=100, H=64,
+           dk=576, dv=512, dt=hs.HS_BF16, scale=0.0, window=16, first=2, sink=None)
+FWD = dict(ATT, out=256, lse=256, stream=None)
+BWD = dict(ATT, out=256, lse=256, dout=256, dq=256, dkey=256, dval=256, dsink=None, ws=256, wsb=1 << 40, stream=None)
+COMMON = [(dict(window=0), INV), (dict(window=-3), INV), (dict(first=-1), INV), (dict(q=None), INV), (dict(k=None), INV),
+          (dict(v=None), INV), (dict(cu=None), INV), (dict(T=-1), INV), (dict(nd=0), INV), (dict(maxlen=0), INV),
+          (dict(H=0), UNS), (dict(H=129), UNS), (dict(dk=0), UNS), (dict(dk=2000), UNS), (dict(dv=0), UNS),
+          (dict(dt=7), UNS), (dict(qhs=5), INV), (dict(qrs=576), INV), (dict(krs=5), INV), (dict(vrs=5), INV),
+          (dict(scale=float("nan")), INV), (dict(out=None), INV), (dict(lse=None), INV)]
+
+
+@pytest.mark.parametrize("kw,code", COMMON)
+def test_window_first_forward_refuses(kw, code):
+    assert _call("hs_swa_first_mqa_fwd", FWD, kw) == code
+
+
+@pytest.mark.parametrize("kw,code", COMMON + [(dict(dout=None), INV), (dict(dq=None), INV), (dict(dkey=None), INV),
+                                              (dict(dval=None), INV), (dict(ws=None), WSP), (dict(wsb=1000), WSP),
+                                              (dict(ws=258), INV)])
+def test_window_first_backward_refuses(kw, code):
+    assert _call("hs_swa_first_mqa_bwd", BWD, kw) == code
+
+
+TABLE = dict(table=256, stride=4, width=4, pages=10, page=16)
+APPEND = dict(k=256, krs=576, v=256, vrs=512, kc=256, vc=256, **TABLE, cu=256, lens=256, S=2, T=5, dk=576, dv=512,
+              dt=hs.HS_BF16, stream=None)
+READ = dict(cache=256, dim=576, **TABLE, cu=256, lens=256, S=2, T=5, out=256, ors=576, dt=hs.HS_BF16, stream=None)
+DECODE = dict(q=256, qrs=64 * 576, qhs=576, kc=256, vc=256, **TABLE, lens=256, S=2, maxlen=64, H=64, dk=576, dv=512,
+              dt=hs.HS_BF16, scale=0.0, window=0, first=0, sink=None, out=256, lse=256, ws=256, wsb=1 << 40, stream=None)
+PAGED = [(dict(page=8), UNS), (dict(page=48), UNS), (dict(pages=-1), INV), (dict(S=-1), INV), (dict(table=None), INV),
+         (dict(width=0), INV), (dict(stride=3), INV), (dict(dt=2), UNS), (dict(lens=None), INV)]
+
+
+@pytest.mark.parametrize("kw,code", PAGED + [
+    (dict(T=-1), INV), (dict(S=0), INV), (dict(cu=None), INV), (dict(dk=48), UNS), (dict(dk=0), UNS),
+    (dict(dk=1056), UNS), (dict(dv=40), UNS), (dict(k=None), INV), (dict(kc=None), INV), (dict(v=None), INV),
+    (dict(vc=None), INV), (dict(dv=0), INV), (dict(krs=100), INV), (dict(vrs=100), INV), (dict(kc=264), INV),
+    (dict(vc=264), INV)])
+def test_append_refuses(kw, code):
+    assert _call("hs_kv4_append", APPEND, kw) == code
+
+
+@pytest.mark.parametrize("kw,code", PAGED + [
+    (dict(T=-1), INV), (dict(S=0), INV), (dict(cu=None), INV), (dict(dim=33), UNS), (dict(cache=None), INV),
+    (dict(out=None), INV), (dict(ors=100), INV), (dict(cache=264), INV)])
+def test_read_refuses(kw, code):
+    assert _call("hs_kv4_read", READ, kw) == code
+
+
+@pytest.mark.parametrize("kw,code", PAGED + [
+    (dict(H=0), UNS), (dict(H=129), UNS), (dict(dk=48), UNS), (dict(dv=0), UNS), (dict(dv=1056), UNS),
+    (dict(q=None), INV), (dict(kc=None), INV), (dict(out=None), INV), (dict(lse=None), INV), (dict(maxlen=0), INV),
+    (dict(vc=None, dv=608), INV), (dict(qhs=100), INV), (dict(qrs=576), INV), (dict(scale=float("inf")), INV),
+    (dict(window=-1), INV), (dict(first=-1), INV), (dict(first=3), INV), (dict(kc=264), INV), (dict(vc=264), INV),
+    (dict(ws=None), WSP), (dict(wsb=16), WSP), (dict(ws=264), INV), (dict(S=2 ** 30), UNS)])
+def test_decode_refuses(kw, code):
+    assert _call("hs_kv4_mqa_decode", DECODE, kw) == code
+
+
+def test_nothing_to_do_is_no_error():
+    assert _call("hs_swa_first_mqa_fwd", FWD, dict(T=0, nd=0, maxlen=0)) == hs.HS_OK
+    assert _call("hs_kv4_append", APPEND, dict(T=0, S=0)) == hs.HS_OK
+    assert _call("hs_kv4_read", READ, dict(T=0, S=0)) == hs.HS_OK
+    assert _call("hs_kv4_mqa_decode", DECODE, dict(S=0, maxlen=0, ws=None)) == hs.HS_OK
+
+
+def test_page_bytes():
+    assert hs.kv4_page_bytes(32, 16) == 16 * 20
+    assert hs.kv4_page_bytes(512, 64) == 64 * (256 + 16)  # 4.25 bits an element
+    assert hs.kv4_page_bytes(576, 128) == 128 * (288 + 20)
+    for width, page in ((0, 16), (33, 16), (1056, 16), (64, 0), (64, 24), (64, 256)):
+        with pytest.raises(ValueError):
+            hs.kv4_page_bytes(width, page)
+
+
+def test_binding_refuses_cpu_tensors():
+    q, k, i = torch.zeros(4, 2, 32), torch.zeros(4, 32), torch.zeros(2, dtype=torch.int32)
+    c = torch.zeros((3, 16 * 20), dtype=torch.uint8)
+    with pytest.raises(ValueError):
+        hs.hs_swa_first_mqa_fwd(q, k, k, i, 4, 2, 1)
+    with pytest.raises(ValueError):
+        hs.hs_kv4_append(k, None, c, None, i[:1, None], i, i[:1], 16)
+    with pytest.raises(ValueError):
+        hs.hs_kv4_mqa_decode(q, c, None, torch.zeros((4, 1), dtype=torch.int32), torch.zeros(4, dtype=torch.int32), 4,
+                             16, 32)

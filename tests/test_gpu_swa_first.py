@@ -1,0 +1,227 @@
+"""hs_swa_first_mqa_fwd / _bwd against a dense-mask form in float64
+(tests/attn64.py, which also gives the error bounds), and against the oracle."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle.hysparse as O
+from block_sparse_mqa_b200 import hs, synth
+from tests import attn64 as A
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+def _inputs(docs, H, dk, dv, dtype, seed):
+    inp = synth.make_inputs(sum(docs), H, dk, dv, dtype=dtype, seed=seed, device=DEV, doc_lengths=docs)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed + 77)
+    dout = torch.randn((sum(docs), H, dv), generator=g, device=DEV).to(dtype)
+    return inp, dout
+
+
+def _check_fwd(inp, W, F, sink, out, lse, dtype, rows=slice(None)):
+    cu = inp.cu_seqlens.tolist()
+    scale = inp.q.shape[2] ** -0.5
+    mask = A.mask_of(cu, W, F, DEV)[rows]
+    ref, rlse, bo, bl = A.forward(inp.q[rows], inp.k, inp.v, mask, sink, scale, dtype)
+    A.check(out[rows], ref, bo, "out")
+    A.check(lse[rows], rlse, bl, "lse")
+
+
+def _check_bwd(inp, W, F, sink, out, lse, dout, grads, dtype):
+    ref = A.backward(inp.q, inp.k, inp.v, out, lse, dout, A.mask_of(inp.cu_seqlens.tolist(), W, F, DEV), sink,
+                     inp.q.shape[2] ** -0.5, dtype)
+    for g, name in zip(grads, ("dq", "dk", "dv", "dsink")):
+        if name in ref:
+            assert g.dtype == (F32 if name == "dsink" else dtype)
+            A.check(g, *ref[name], name)
+        else:
+            assert g is None
+
+
+def _run(docs, H, dk, dv, dtype, W, F, with_sink=True, seed=0, grad=True, path=None):
+    inp, dout = _inputs(docs, H, dk, dv, dtype, seed)
+    sink = inp.sink if with_sink else None
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, inp.max_seqlen, W, F, sink)
+    if path is not None:
+        assert hs.last_path() == path[0]
+    hs.poll_status()
+    _check_fwd(inp, W, F, sink, out, lse, dtype)
+    if grad:
+        g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, inp.cu_seqlens, inp.max_seqlen, W, F, out, lse, dout, sink)
+        if path is not None:
+            assert hs.last_path() == path[1]
+        hs.poll_status()
+        _check_bwd(inp, W, F, sink, out, lse, dout, g, dtype)
+
+
+WF = [(1, 0), (1, 1), (3, 2), (40, 5), (16, 200), (1000, 7), (2 ** 31 - 1, 2 ** 31 - 1)]
+
+
+@pytest.mark.parametrize("W,F", WF)
+def test_fp32(W, F):
+    _run([97, 40, 1, 150], 4, 64, 48, F32, W, F, with_sink=W != 40)
+
+
+@pytest.mark.parametrize("H,dk,dv", [(1, 1, 1), (3, 40, 24), (5, 33, 70)])
+def test_odd_shapes(H, dk, dv):
+    for dtype in (F32, BF16):
+        _run([33, 2, 60], H, dk, dv, dtype, 9, 3)
+
+
+@pytest.mark.parametrize("W,F", WF + [(100, 4), (128, 128), (129, 130), (124, 4), (120, 8), (250, 6)])
+def test_mla_shape(W, F):
+    _run([130, 64, 1, 257], 64, 576, 512, BF16, W, F, with_sink=F != 5, seed=1)
+
+
+@pytest.mark.parametrize("dk,dv", [(512, 512), (192, 128), (64, 64), (576, 448), (256, 320)])
+@pytest.mark.parametrize("W,F", [(30, 4), (200, 17)])
+def test_widths(dk, dv, W, F):
+    _run([150, 290], 64, dk, dv, BF16, W, F, seed=2)
+
+
+@pytest.mark.parametrize("docs", [[1], [2], [0, 3, 0], [127], [128], [129, 1], [5] * 60])
+def test_document_lengths(docs):
+    _run(docs, 64, 128, 128, BF16, 6, 2, seed=3)
+
+
+def test_several_query_ranges_of_the_backward():
+    """A document longer than the backward's query ranges: its first keys get
+    gradients from all of them."""
+    docs, W, F = [1300, 700], 33, 40
+    _run(docs, 64, 64, 64, BF16, W, F, seed=4)
+
+
+def test_matches_the_oracle():
+    docs, W, F = [90, 41], 20, 3
+    inp, _ = _inputs(docs, 64, 576, 512, BF16, 5)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, inp.max_seqlen, W, F, inp.sink)
+    n = lambda t: t.double().cpu().numpy()
+    ref = O.swa_first_mqa_fwd(n(inp.q), n(inp.k), n(inp.v), inp.cu_seqlens.tolist(), W, F, n(inp.sink))
+    # out: two roundings of at most 2^-8 over values of size |v| <= 6
+    assert np.abs(n(out) - ref["out"]).max() <= 6 * 2 * 2.0 ** -8
+    assert np.abs(n(lse) - ref["lse"]).max() <= 1e-4
+
+
+@pytest.mark.parametrize("shape", [(64, 576, 512), (64, 192, 128), (4, 64, 48)])
+def test_nothing_outside_the_key_set_is_used(shape):
+    """NaN and infinities between the first tokens and the window, behind the
+    query and in other documents; q of the poisoned tokens stays finite."""
+    docs, W, F, bad = [200, 150, 60], 20, 5, [30, 31, 77, 128, 260, 350, 351, 409]
+    inp, dout = _inputs(docs, *shape, BF16, 6)
+    cu = inp.cu_seqlens.tolist()
+    for i, t in enumerate(bad):
+        inp.k[t], inp.v[t] = (float("nan"), float("inf")) if i % 2 else (float("-inf"), float("nan"))
+    mask = A.mask_of(cu, W, F, DEV)
+    clean = ~mask[:, bad].any(1)
+    assert 200 < int(clean.sum()) < sum(docs)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, inp.max_seqlen, W, F, inp.sink)
+    hs.poll_status()
+    _check_fwd(inp, W, F, inp.sink, out, lse, BF16, rows=clean)
+    # the backward of the rows that stay clean: the other rows are given finite
+    # outputs and zero probabilities
+    out[~clean], lse[~clean] = 0, float("inf")
+    dq = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, inp.cu_seqlens, inp.max_seqlen, W, F, out, lse, dout, inp.sink)[0]
+    hs.poll_status()
+    ref = A.backward(inp.q[clean], inp.k, inp.v, out[clean], lse[clean], dout[clean], mask[clean], inp.sink,
+                     shape[1] ** -0.5, BF16)
+    A.check(dq[clean], *ref["dq"], "dq")
+
+
+def test_strided_and_aliased_inputs():
+    docs, W, F = [140, 75], 50, 4
+    T = sum(docs)
+    base, dout = _inputs(docs, 64, 576, 512, BF16, 7)
+    for pad, offset in ((8, 0), (16, 8), (3, 1)):  # the last one is not 16-byte aligned
+        q = torch.zeros((T, 66, 576 + pad), device=DEV, dtype=BF16)[:, 1:65, offset:offset + 576]
+        kv = torch.zeros((T, 576 + pad), device=DEV, dtype=BF16)[:, offset:offset + 576]
+        q.copy_(base.q)
+        kv.copy_(base.k)
+        v = kv[:, :512]  # the latent part of the keys
+        out, lse = hs.hs_swa_first_mqa_fwd(q, kv, v, base.cu_seqlens, 140, W, F, base.sink)
+        g = hs.hs_swa_first_mqa_bwd(q, kv, v, base.cu_seqlens, 140, W, F, out, lse, dout, base.sink)
+        hs.poll_status()
+        base.v = v
+        _check_fwd(base, W, F, base.sink, out, lse, BF16)
+        _check_bwd(base, W, F, base.sink, out, lse, dout, g, BF16)
+
+
+def test_wide_window_equals_the_window_call():
+    docs = [129, 300]
+    inp, _ = _inputs(docs, 64, 192, 128, BF16, 8)
+    a = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 300, 64, 0, inp.sink)
+    b = hs.hs_swa_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 300, 64, inp.sink)
+    # both are within the bound of the same values; the roundings are at most two of 2^-8 each
+    assert (a[0].float() - b[0].float()).abs().max() <= 4 * 2.0 ** -8 * inp.v.abs().max()
+    assert (a[1] - b[1]).abs().max() <= 1e-4
+
+
+@pytest.mark.parametrize("shape,dtype", [((64, 576, 512), BF16), ((4, 64, 48), F32)])
+def test_deterministic_on_another_stream_and_in_a_graph(shape, dtype):
+    docs, W, F = [200, 333], 60, 4
+    inp, dout = _inputs(docs, *shape, dtype, 9)
+    args = (inp.cu_seqlens, inp.max_seqlen, W, F)
+
+    def step():
+        out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+        return (out, lse) + tuple(hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink))
+
+    want = [x.clone() for x in step()]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    again = torch.randn_like(inp.q)
+    keep = inp.q.clone()
+    inp.q.copy_(again)
+    graph.replay()
+    moved = [x.clone() for x in held]
+    fresh = step()
+    inp.q.copy_(keep)
+    graph.replay()
+    hs.poll_status()
+    for a, b, c, d, e in zip(want, other, held, moved, fresh):
+        assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(d, e)
+
+
+def test_huge_logits_and_rows_without_weight():
+    """Logits of +-3e4 (one key takes everything, others underflow) and a sink
+    that takes everything."""
+    docs, W, F = [260], 70, 4
+    inp, _ = _inputs(docs, 64, 192, 128, BF16, 10)
+    inp.q.mul_(1000)
+    inp.sink.fill_(2.0)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 260, W, F, inp.sink)
+    hs.poll_status()
+    _check_fwd(inp, W, F, inp.sink, out, lse, BF16)
+    inp.sink.fill_(1e6)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 260, W, F, inp.sink)
+    assert not out.any() and torch.equal(lse, torch.full_like(lse, 1e6))
+
+
+def test_malformed_documents_are_reported():
+    inp, _ = _inputs([64, 64], 64, 64, 64, BF16, 11)
+    out = torch.full((128, 64, 64), 7.0, device=DEV, dtype=BF16)
+    cu = torch.tensor([0, 64, 100], device=DEV, dtype=torch.int32)  # the last 28 rows are in no document
+    hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, cu, 64, 8, 2, inp.sink, out=out)
+    with pytest.raises(hs.HSError) as e:
+        hs.poll_status()
+    assert e.value.status == hs.HS_ERR_INVALID_ARG
+    assert bool((out[100:] == 7).all()) and not bool((out[:100] == 7).all())
+
+
+def test_no_tokens():
+    q = torch.zeros((0, 64, 576), device=DEV, dtype=BF16)
+    k, v = q[:, 0], q[:, 0, :512]
+    cu, sink = torch.zeros(1, device=DEV, dtype=torch.int32), torch.zeros(64, device=DEV)
+    out, lse = hs.hs_swa_first_mqa_fwd(q, k, v, cu, 1, 4, 1, sink)
+    assert out.shape == (0, 64, 512) and lse.shape == (0, 64)
+    g = hs.hs_swa_first_mqa_bwd(q, k, v, cu, 1, 4, 1, out, lse, out, sink)
+    assert g[0].shape == (0, 64, 576) and not g[3].any()
