@@ -8,6 +8,7 @@
 #include <stdio.h>
 #include <string.h>
 
+#include <algorithm>
 #include <atomic>
 #include <mutex>
 
@@ -207,8 +208,11 @@ int hs_path(int op, hs_dtype dtype, int num_heads, int dk, int dv, int block_siz
         return HS_PATH_TCGEN05;
       return HS_PATH_SIMT;
     case HS_OP_SWA_FIRST_MQA:
-    case HS_OP_SWA_FIRST_MQA_BWD:
-    case HS_OP_KV4_MQA_DECODE: return HS_PATH_SIMT;
+    case HS_OP_SWA_FIRST_MQA_BWD: return HS_PATH_SIMT;
+    case HS_OP_KV4_MQA_DECODE:
+      return !g_force_simt.load() && hs::tc_kv4_decode_shape_ok(num_heads, dk, dv, dtype)
+                 ? HS_PATH_TCGEN05
+                 : HS_PATH_SIMT;
     case HS_OP_SPARSE_MQA_BWD:
     case HS_OP_SWA_MQA_BWD:
       if (!g_force_simt.load() && hs::tc_backward_shape_ok(dtype, num_heads, dk, dv))
@@ -230,7 +234,10 @@ size_t hs_workspace_size(int op, int total_tokens, int num_docs, int max_seqlen,
                          int dk, int dv, hs_dtype dtype, int block_size) {
   if (op == HS_OP_KV4_MQA_DECODE) {  // total_tokens = the number of sequences
     if (total_tokens <= 0 || num_heads <= 0 || dv <= 0) return 0;
-    return hs::simt_kv4_decode_workspace(total_tokens, num_heads, max_seqlen, dv);
+    size_t need = hs::simt_kv4_decode_workspace(total_tokens, num_heads, max_seqlen, dv);
+    if (!g_force_simt.load() && hs::tc_kv4_decode_shape_ok(num_heads, dk, dv, dtype))
+      need = std::max(need, hs::tc_kv4_decode_workspace(total_tokens, num_heads, dv));
+    return need;
   }
   if ((op == HS_OP_SPARSE_MQA_BWD || op == HS_OP_SWA_MQA_BWD || op == HS_OP_SWA_FIRST_MQA_BWD) &&
       total_tokens > 0 && num_heads > 0)
@@ -866,6 +873,9 @@ hs_status hs_kv4_mqa_decode(const void* q, int64_t q_row_stride, int64_t q_head_
   a.workspace = workspace;
   r = status_ptr(&a.status);
   if (r != HS_OK) return r;
+  if (!g_force_simt.load() && hs::tc_kv4_decode_eligible(a))
+    return launched_on(hs::launch_tc_kv4_decode(a, g_wait_limit.load(), stream),
+                       "tc 4-bit cache decode", HS_PATH_TCGEN05);
   return launched_on(hs::launch_simt_kv4_decode(a, stream), "simt 4-bit cache decode",
                      HS_PATH_SIMT);
 }

@@ -174,6 +174,10 @@ cudaError_t launch_kv4_read(const Kv4Rows& a, const void* cache, int width, void
                             int64_t out_row_stride, hs_dtype dtype, cudaStream_t s);
 size_t simt_kv4_decode_workspace(int num_seqs, int num_heads, int max_seqlen, int dv);
 cudaError_t launch_simt_kv4_decode(const Kv4Decode& a, cudaStream_t s);
+bool tc_kv4_decode_shape_ok(int num_heads, int dk, int dv, hs_dtype dtype);
+bool tc_kv4_decode_eligible(const Kv4Decode& a);
+size_t tc_kv4_decode_workspace(int num_seqs, int num_heads, int dv);
+cudaError_t launch_tc_kv4_decode(const Kv4Decode& a, long long wait_limit, cudaStream_t s);
 
 // Records msg as the calling thread's hs_last_error() and returns st.
 hs_status report_error(hs_status st, const char* msg);
