@@ -55,7 +55,7 @@ constexpr int kHG = 64;                // heads per pass
 constexpr int kPanel = 16384;          // 128 keys x 64 columns bf16
 constexpr int kQChunk = kHG * 128;     // 64 heads x 64 columns bf16
 constexpr int kPBytes = kTile * 128;   // P^T: 128 keys x 64 heads bf16
-constexpr int kSteps = 5;              // K expansion steps of 128 columns (Dk <= 576)
+constexpr int kSteps = 5;              // runs of four groups (128 columns) of a key (Dk <= 576)
 constexpr int kSCol = 256;             // TMEM: O^T in columns 0..255, S^T behind
 constexpr int kMaxCtas = 148;          // workspace slots (a constant of the sizes alone)
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -67,6 +67,7 @@ struct Params {
   int nck, nvp, nvc;   // K panels, V panels, 128-row V chunks
   int groups, ctas;    // head groups, CTAs of one head group
   int panels;          // panels in shared memory
+  int qrows;           // heads of a Q box
   int own_p;           // P^T has its own place (else the ninth panel's)
   float scale_log2;
   int* prefix;         // [num_seqs + 1] first tile of each sequence
@@ -76,7 +77,7 @@ struct Params {
 };
 
 struct Shared {
-  uint64_t kfull[kSteps], vfull[4], pvchunk[4];
+  uint64_t kfull[4], vfull[4], pvchunk[4], qfull;
   uint64_t sfull, pfull, drain[2];
   uint64_t rv[4], seg;        // the 4 warps of a head quarter meet; all 16 after a segment
   float mrun[kHG], alpha[kHG], inv[kHG];
@@ -102,12 +103,13 @@ __device__ __forceinline__ int tiles_of(int n) { return (n + kTile - 1) / kTile;
 // 32 codes and their scale -> 32 bf16 as four 16-byte units of row `row` of a
 // panel (128 bytes per row, 128-byte swizzle), units 4 * half ...  A code
 // n becomes the bf16 number 128 + n by setting its bits under the exponent of
-// 128; 136 off gives n - 8, and the product with the scale is exact.
+// 128; (128 + n) s - 136 s is one fma, exact because 136 s = 17 s * 8 still
+// fits bf16 (17 * 15 < 2^8).
 __device__ __forceinline__ void expand(uint8_t* panel, int row, int half, uint4 codes,
                                        uint32_t byte) {
   const uint32_t word[4] = {codes.x, codes.y, codes.z, codes.w};
-  const __nv_bfloat162 s2 = __float2bfloat162_rn(kv4::scale_value(byte));
-  const __nv_bfloat162 c136 = __float2bfloat162_rn(136.f);
+  const float sf = kv4::scale_value(byte);
+  const __nv_bfloat162 s2 = __float2bfloat162_rn(sf), z2 = __float2bfloat162_rn(-136.f * sf);
   uint8_t* r = panel + row * 128;
 #pragma unroll
   for (int w = 0; w < 4; ++w) {
@@ -115,9 +117,8 @@ __device__ __forceinline__ void expand(uint8_t* panel, int row, int half, uint4 
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
       const uint32_t t = ((word[w] >> (4 * k)) & 0x000f000fu) | 0x43004300u;
-      __nv_bfloat162 v = *reinterpret_cast<const __nv_bfloat162*>(&t);
-      v = __hmul2(__hsub2(v, c136), s2);
-      o[k] = *reinterpret_cast<uint32_t*>(&v);
+      const __nv_bfloat162 v = __hfma2(*reinterpret_cast<const __nv_bfloat162*>(&t), s2, z2);
+      o[k] = *reinterpret_cast<const uint32_t*>(&v);
     }
     *reinterpret_cast<uint4*>(r + (((4 * half + w) ^ (row & 7)) << 4)) =
         make_uint4(o[0], o[1], o[2], o[3]);
@@ -134,16 +135,36 @@ template <int N>
 __device__ __forceinline__ void load_codes(Codes<N>& d, const uint8_t* cache, int width,
                                            int ps_log2, int page, int slot, int hq) {
   const int G = kv4::groups(width), ps = 1 << ps_log2;
-  const uint8_t* pg = cache + (int64_t)max(page, 0) * kv4::page_bytes(width, ps);
+  const uint8_t* pg = cache + (int64_t)page * kv4::page_bytes(width, ps) + slot * 16;
+  const uint8_t* sc = pg + G * ps * 16 - slot * 12;
 #pragma unroll
   for (int j = 0; j < N; ++j) {
     d.c[j] = make_uint4(0u, 0u, 0u, 0u);
     d.s[j] = 0u;
     if (page >= 0 && 4 * j + hq < G) {
-      d.c[j] = __ldg(reinterpret_cast<const uint4*>(pg + kv4::code_off(4 * j + hq, slot, ps)));
-      d.s[j] = __ldg(reinterpret_cast<const uint32_t*>(pg + kv4::scale_off(4 * j, slot, ps, G)));
+      d.c[j] = __ldg(reinterpret_cast<const uint4*>(pg + (4 * j + hq) * ps * 16));
+      d.s[j] = __ldg(reinterpret_cast<const uint32_t*>(sc + j * ps * 4));
     }
   }
+}
+
+// Lane 2h and 2h + 1 receive op over the 32 lanes of v[h].
+template <bool kMax>
+__device__ __forceinline__ float reduce16(float (&v)[16]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16; off >= 2; off >>= 1) {
+    const bool upper = (lane & off) != 0;
+#pragma unroll
+    for (int j = 0; j < off / 2; ++j) {
+      const float send = upper ? v[j] : v[j + off / 2];
+      const float keep = upper ? v[j + off / 2] : v[j];
+      const float got = __shfl_xor_sync(0xffffffffu, send, off);
+      v[j] = kMax ? fmaxf(keep, got) : keep + got;
+    }
+  }
+  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
+  return kMax ? fmaxf(v[0], got) : v[0] + got;
 }
 
 // Bounded wait of a whole warp: all its lanes go on, or all give up.
@@ -170,7 +191,8 @@ __device__ __forceinline__ void publish(uint64_t* bar, int lane) {
 }
 
 template <bool kAlias>
-__global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid_constant__ Params p) {
+__global__ void __launch_bounds__(kThreads, 1)
+tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~static_cast<uintptr_t>(1023));
@@ -186,13 +208,14 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
   const long long lim = p.wait_ns;
 
   if (tid == 0) {
-    for (int i = 0; i < kSteps; ++i) mbar_init(&sh->kfull[i], 16);
     for (int i = 0; i < 4; ++i) {
+      mbar_init(&sh->kfull[i], 16);
       mbar_init(&sh->vfull[i], 16);
       mbar_init(&sh->pvchunk[i], 1);
       mbar_init(&sh->rv[i], 4);
       sh->flag[i][0] = sh->flag[i][1] = 0;
     }
+    mbar_init(&sh->qfull, 1);
     mbar_init(&sh->sfull, 1);
     mbar_init(&sh->pfull, 16);
     mbar_init(&sh->seg, 16);
@@ -256,26 +279,24 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
       const uint64_t q_desc = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
       const uint64_t v_desc = umma_desc_sw128(smem_u32(panels), kPanel, 1024);
       const uint64_t p_desc = umma_desc_sw128(smem_u32(pbuf), kPanel, 1024);
-      uint32_t ph = 0;
+      uint32_t ph = 0, qph = 0;
       bool ok = true;
       for (; left > 0 && ok; ++b, ta = 0) {
         const int tb = min(tiles_of(seq_keys(a, b).n), ta + left);
         for (int i = ta; i < tb && ok; ++i, ph ^= 1) {
           if (!is_pv) {
-            for (int j = 0; 2 * j < p.nck; ++j) {
-              if (!mbar_wait_spin(&sh->kfull[j], ph, lim)) { ok = false; break; }
-              tc_fence_after();
-              const uint64_t ka = k_desc + (uint64_t)((2 * j * kPanel) >> 4);
-              const uint64_t qa = q_desc + (uint64_t)((2 * j * kQChunk) >> 4);
+            if (i == ta && !mbar_wait_spin(&sh->qfull, qph, lim)) { ok = false; break; }
+            for (int c = 0; c < p.nck; ++c) {
+              // step j brought panels 2j, 2j + 1; the last one the ninth, too
+              if (!(c & 1) && c < 8) {
+                if (!mbar_wait_spin(&sh->kfull[c >> 1], ph, lim)) { ok = false; break; }
+                tc_fence_after();
+              }
+              const uint64_t ka = k_desc + (uint64_t)((c * kPanel) >> 4);
+              const uint64_t qa = q_desc + (uint64_t)((c * kQChunk) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                umma_ss(tmem + kSCol, ka + 2 * k, qa + 2 * k, id_qk, (j > 0 || k > 0) ? 1u : 0u);
-              if (2 * j + 1 < p.nck) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                  umma_ss(tmem + kSCol, ka + (kPanel >> 4) + 2 * k, qa + (kQChunk >> 4) + 2 * k,
-                          id_qk, 1u);
-              }
+                umma_ss(tmem + kSCol, ka + 2 * k, qa + 2 * k, id_qk, (c > 0 || k > 0) ? 1u : 0u);
             }
             if (ok) umma_commit(&sh->sfull);
           } else {
@@ -295,6 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
             }
           }
         }
+        if (tb > ta) qph ^= 1;
         left -= tb - ta;
       }
       if (!ok) record_status(a.status, HS_ERR_TIMEOUT);
@@ -313,34 +335,35 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
     bool ok = true, any_pv = false, first_seg = true;
     Codes<kSteps> kc;
     Codes<4> vc;
-    auto page_at = [&](const kv4::KeyList& kl, int bb, int tile, int& slot) -> int {
+    int slot = 0;
+    // The table entry of this thread's key of a tile, loaded a tile ahead and
+    // checked where it is used.
+    auto entry_at = [&](const kv4::KeyList& kl, int bb, int tile) -> int {
       const int x = tile * kTile + r;
       if (x >= kl.n) return -1;
-      const int pos = kl.pos(x);
-      slot = pos & ((1 << a.ps_log2) - 1);
-      return kv4::page_of(a.table + (int64_t)bb * a.table_stride, a.table_width, a.num_pages, pos,
-                          a.ps_log2, a.status);
+      const int e = kl.pos(x) >> a.ps_log2;
+      return e < a.table_width ? __ldg(a.table + (int64_t)bb * a.table_stride + e) : -1;
+    };
+    auto load_k = [&](const kv4::KeyList& kl, int tile, int& page) {
+      if ((unsigned)page >= (unsigned)a.num_pages) {
+        if (tile * kTile + r < kl.n) record_status(a.status, HS_ERR_INVALID_INDEX);
+        page = -1;
+      }
+      slot = kl.pos(tile * kTile + r) & ((1 << a.ps_log2) - 1);
+      load_codes(kc, a.k_cache, a.dk, a.ps_log2, page, slot, hq);
     };
     for (; left > 0 && ok; ++b, ta = 0) {
       const kv4::KeyList kl = seq_keys(a, b);
       const int nt = tiles_of(kl.n), tb = min(nt, ta + left);
       if (tb == ta) continue;  // an empty sequence
-      int slot = 0, page = page_at(kl, b, ta, slot);
-      load_codes(kc, a.k_cache, a.dk, a.ps_log2, page, slot, hq);
-      if (!kAlias) load_codes(vc, a.v_cache, a.dv, a.ps_log2, page, slot, hq);
-      if (ta + 1 < tb) page = page_at(kl, b, ta + 1, slot);
-      // Q of this sequence (every QK of the one before is complete)
-      {
-        const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(a.q) +
-                                 (int64_t)b * a.q_row_stride + (int64_t)h0 * a.q_head_stride;
-        const int units = p.nck * 8;  // 16-byte units of a head
-        for (int e = tid; e < hn * units; e += kWorkers) {
-          const int h = e / units, u = e - h * units;
-          *reinterpret_cast<uint4*>(qbuf + (u >> 3) * kQChunk + h * 128 +
-                                    (((u & 7) ^ (h & 7)) << 4)) =
-              __ldg(reinterpret_cast<const uint4*>(q + (int64_t)h * a.q_head_stride) + u);
-        }
+      if (tid == 0) {  // Q (every QK of the sequence before is complete)
+        mbar_expect_tx(&sh->qfull, p.nck * p.qrows * 128);
+        for (int c = 0; c < p.nck; ++c)
+          tma_load_3d(qbuf + c * kQChunk, &qmap, &sh->qfull, c * 64, h0, b);
       }
+      int page = entry_at(kl, b, ta), next = ta + 1 < tb ? entry_at(kl, b, ta + 1) : -1;
+      load_k(kl, ta, page);
+      if (!kAlias) load_codes(vc, a.v_cache, a.dv, a.ps_log2, page, slot, hq);
       float lpart[16];
 #pragma unroll
       for (int k = 0; k < 16; ++k) lpart[k] = 0.f;
@@ -348,19 +371,27 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
         // ---- K panels 2j, 2j + 1 of this tile, once PV of the tile before
         // has read them (and P^T, for the ninth)
 #pragma unroll
-        for (int j = 0; j < kSteps; ++j) {
+        for (int j = 0; j < 4; ++j) {
           if (2 * j >= p.nck) break;
           const int c = min(j, p.nvc - 1);
           if (any_pv && !warp_wait(&sh->pvchunk[c], ph ^ 1, lim)) { ok = false; break; }
           const int g = 4 * j + hq;
           if (g < 2 * p.nck)
             expand(panels + (g >> 1) * kPanel, r, g & 1, kc.c[j], (kc.s[j] >> (8 * hq)) & 0xffu);
+          if (j == 3 && p.nck == 9) {
+            if (any_pv && !warp_wait(&sh->pvchunk[p.nvc - 1], ph ^ 1, lim)) { ok = false; break; }
+            if (hq < 2)
+              expand(panels + 8 * kPanel, r, hq, kc.c[4], (kc.s[4] >> (8 * hq)) & 0xffu);
+          }
           publish(&sh->kfull[j], lane);
         }
         if (!ok) break;
-        // the next tile's codes, then the page of the one after
-        if (i + 1 < tb) load_codes(kc, a.k_cache, a.dk, a.ps_log2, page, slot, hq);
-        if (kAlias && i + 2 < tb) page = page_at(kl, b, i + 2, slot);
+        // the next tile's codes, the table entry of the one after
+        if (i + 1 < tb) {
+          page = next;
+          next = i + 2 < tb ? entry_at(kl, b, i + 2) : -1;
+          load_k(kl, i + 1, page);
+        }
         // ---- softmax: row r of S^T, heads hb .. hb + 15
         if (!warp_wait(&sh->sfull, ph, lim)) { ok = false; break; }
         // PV of the tile before has read P^T (and V) and added to O^T
@@ -373,14 +404,18 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
           tmem_ld_wait();
           reg_fence(u);
           const bool valid = i * kTile + r < kl.n;
-          const volatile float* const mr = sh->mrun + hb;
+          const float4* const mr = reinterpret_cast<const float4*>(sh->mrun + hb);
           float x[16];
-          bool over = first;
+          float most = -INFINITY;  // above the running maximum
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            x[k] = valid ? __uint_as_float(u[k]) * sl2 : -INFINITY;
-            over = over || x[k] > mr[k] + kRescaleLog2;
+          for (int k = 0; k < 16; ++k) x[k] = valid ? __uint_as_float(u[k]) * sl2 : -INFINITY;
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float4 m = mr[k];
+            most = fmaxf(most, fmaxf(fmaxf(x[4 * k] - m.x, x[4 * k + 1] - m.y),
+                                     fmaxf(x[4 * k + 2] - m.z, x[4 * k + 3] - m.w)));
           }
+          bool over = first || most > kRescaleLog2;
           const int par = i & 1;
           if (!first) {
             if (__any_sync(0xffffffffu, over) && lane == 0) sh->flag[hq][par] = 1;
@@ -391,13 +426,11 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
             sh->flag[hq][0] = sh->flag[hq][1] = 0;  // read next after two rendezvous
           }
           if (over) {  // the tile's maximum per head joins the running one
-            float mine16 = -INFINITY;
+            float y[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const float wm = warp_max(x[k]);
-              if (lane == k) mine16 = wm;
-            }
-            if (lane < 16) sh->red[hq][g4][lane] = mine16;
+            for (int k = 0; k < 16; ++k) y[k] = x[k];
+            const float wm = reduce16<true>(y);
+            if (!(lane & 1)) sh->red[hq][g4][lane >> 1] = wm;
             if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
             if (g4 == 0 && lane < 16) {
               const float tm = fmaxf(fmaxf(sh->red[hq][0][lane], sh->red[hq][1][lane]),
@@ -416,15 +449,22 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
             for (int k = 0; k < 16; ++k) lpart[k] *= sh->alpha[hb + k];
           }
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
+          for (int k = 0; k < 4; ++k) {
             // every logit so far -inf: exp2(-inf - 0) = 0
-            const float m0 = mr[2 * k], m1 = mr[2 * k + 1];
-            const float e0 = fast_exp2(x[2 * k] - (m0 == -INFINITY ? 0.f : m0));
-            const float e1 = fast_exp2(x[2 * k + 1] - (m1 == -INFINITY ? 0.f : m1));
-            lpart[2 * k] += e0;
-            lpart[2 * k + 1] += e1;
-            __nv_bfloat162 pr = __floats2bfloat162_rn(e0, e1);
-            pk[k] = *reinterpret_cast<uint32_t*>(&pr);
+            float4 m = mr[k];
+            m.x = m.x == -INFINITY ? 0.f : m.x;
+            m.y = m.y == -INFINITY ? 0.f : m.y;
+            m.z = m.z == -INFINITY ? 0.f : m.z;
+            m.w = m.w == -INFINITY ? 0.f : m.w;
+            const float e0 = fast_exp2(x[4 * k] - m.x), e1 = fast_exp2(x[4 * k + 1] - m.y);
+            const float e2 = fast_exp2(x[4 * k + 2] - m.z), e3 = fast_exp2(x[4 * k + 3] - m.w);
+            lpart[4 * k] += e0;
+            lpart[4 * k + 1] += e1;
+            lpart[4 * k + 2] += e2;
+            lpart[4 * k + 3] += e3;
+            __nv_bfloat162 p0 = __floats2bfloat162_rn(e0, e1), p1 = __floats2bfloat162_rn(e2, e3);
+            pk[2 * k] = *reinterpret_cast<uint32_t*>(&p0);
+            pk[2 * k + 1] = *reinterpret_cast<uint32_t*>(&p1);
           }
           if (resc) {
 #pragma unroll 1
@@ -459,7 +499,6 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
             publish(&sh->vfull[c], lane);
           }
           if (i + 1 < tb) load_codes(vc, a.v_cache, a.dv, a.ps_log2, page, slot, hq);
-          if (i + 2 < tb) page = page_at(kl, b, i + 2, slot);
         }
         any_pv = true;
         ph ^= 1;
@@ -469,13 +508,8 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
       const bool whole = ta == 0 && tb == nt;
       const int64_t slot2 = ((int64_t)group * p.ctas + cta) * 2 + (first_seg ? 0 : 1);
       if (act) {
-        float mine16 = 0.f;
-#pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const float ws = warp_sum(lpart[k]);
-          if (lane == k) mine16 = ws;
-        }
-        if (lane < 16) sh->red[hq][g4][lane] = mine16;
+        const float ws = reduce16<false>(lpart);
+        if (!(lane & 1)) sh->red[hq][g4][lane >> 1] = ws;
         if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
         const int h = h0 + hb + lane;
         if (g4 == 0 && lane < 16 && hb + lane < hn) {
@@ -497,26 +531,30 @@ __global__ void __launch_bounds__(kThreads, 1) tc_kv4_decode_kernel(const __grid
         if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
         if (!warp_wait(&sh->pvchunk[p.nvc - 1], ph ^ 1, lim)) { ok = false; break; }
         tc_fence_after();
+        // rows of a chunk = consecutive d: a warp stores 32 of one head at a
+        // time.  Rolled up on purpose: code that runs once per sequence costs
+        // its instruction fetches.
         const int hc = min(16, hn - hb);
+        __nv_bfloat16* const ob = static_cast<__nv_bfloat16*>(a.out) +
+                                  ((int64_t)b * a.num_heads + h0 + hb) * a.dv;
+        float* const op = p.part_o + (slot2 * kHG + hb) * a.dv;
+#pragma unroll 1
         for (int c = 0; c < p.nvc; ++c) {
-          uint32_t w[16];
-          tmem_ld16(lane_base + c * kHG + hb, w);
-          tmem_ld_wait();
-          reg_fence(w);
           const int d = c * 128 + r;
-          if (d < a.dv) {
-            if (whole) {
-              __nv_bfloat16* o = static_cast<__nv_bfloat16*>(a.out) +
-                                 ((int64_t)b * a.num_heads + h0 + hb) * a.dv + d;
+#pragma unroll 1
+          for (int k = 0; k < hc; k += 8) {
+            uint32_t w[8];
+            tmem_ld8(lane_base + c * kHG + hb + k, w);
+            tmem_ld_wait();
+            reg_fence(w);
 #pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (k < hc)
-                  o[(int64_t)k * a.dv] = __float2bfloat16_rn(__uint_as_float(w[k]) * sh->inv[hb + k]);
-            } else {
-              float* o = p.part_o + (slot2 * kHG + hb) * a.dv + d;
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                if (k < hc) o[(int64_t)k * a.dv] = __uint_as_float(w[k]);
+            for (int e = 0; e < 8; ++e) {
+              if (d >= a.dv || k + e >= hc) continue;
+              const float v = __uint_as_float(w[e]);
+              if (whole)
+                ob[(k + e) * a.dv + d] = __float2bfloat16_rn(v * sh->inv[hb + k + e]);
+              else
+                op[(k + e) * a.dv + d] = v;
             }
           }
         }
@@ -663,13 +701,21 @@ cudaError_t launch_tc_kv4_decode(const Kv4Decode& a, long long wait_limit, cudaS
   p.part_ml = reinterpret_cast<float2*>(w);
   p.part_o = reinterpret_cast<float*>(w + slots * sizeof(float2));
   p.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
+  CUtensorMap qmap;
+  {
+    p.qrows = a.num_heads < kHG ? a.num_heads : kHG;
+    const uint64_t dims[3] = {(uint64_t)a.dk, (uint64_t)a.num_heads, (uint64_t)a.num_seqs};
+    const uint64_t strides[2] = {(uint64_t)a.q_head_stride * 2, (uint64_t)a.q_row_stride * 2};
+    const uint32_t box[3] = {64, (uint32_t)p.qrows, 1};
+    if (!encode_bf16_map(&qmap, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
+  }
   const size_t bytes = 1024 + (size_t)p.panels * kPanel + (size_t)p.nck * kQChunk +
                        (p.own_p ? kPBytes : 0) + sizeof(Shared);
   auto kern = a.v_cache ? tc_kv4_decode_kernel<false> : tc_kv4_decode_kernel<true>;
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  kern<<<p.ctas * p.groups, kThreads, bytes, s>>>(p);
+  kern<<<p.ctas * p.groups, kThreads, bytes, s>>>(qmap, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   tc_kv4_join_kernel<<<dim3(a.num_seqs, (a.num_heads + 7) / 8), 256, 0, s>>>(p);
