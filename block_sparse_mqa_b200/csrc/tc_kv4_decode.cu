@@ -20,14 +20,14 @@
 // One tile's panels (9 x 16 KB), Q (72 KB) and P^T (16 KB) do not fit one
 // SM's 227 KB together; P^T therefore takes the place of the ninth panel,
 // which only S^T reads.  The expansion of tile i + 1 follows PV of tile i
-// 128 columns at a time (step c: panels 2c, 2c + 1 once PV chunk c has read
-// them), and QK of tile i + 1 follows the expansion, so the three overlap;
+// panel by panel (panels 2c, 2c + 1 once PV chunk c has read them), and QK of
+// tile i + 1 follows the expansion, so the three overlap;
 // codes of tile i + 1 wait in registers since before the softmax of tile i.
 // A value plane of its own is expanded into the panels after QK.
 //
-// 16 warps expand and compute the softmax (thread = key row of S^T, 16 heads
-// each); two further warps issue the QK and the PV MMAs.  The running maximum
-// of a head is raised only when a logit passes it by more than 2^8, so a tile
+// 8 warps expand and compute the softmax (thread = key row of S^T, 32 heads);
+// two further warps issue the QK and the PV MMAs.  The running maximum of a
+// head is raised only when a logit passes it by more than 2^8, so a tile
 // usually needs one vote and no reduction.
 //
 // Work: the tiles of all sequences in order are cut into equal ranges, one
@@ -48,14 +48,17 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWorkers = 512;          // 16 warps
+constexpr int kWarps = 8;               // expansion and softmax (16 had 96 registers each, spilled and took 129 us for 106)
+constexpr int kParts = kWarps / 4;    // each part of the warps has 64 / kParts heads
+constexpr int kHP = 64 / kParts;
+constexpr int kPE = 8 / kParts;       // panels of a thread
+constexpr int kWorkers = kWarps * 32;
 constexpr int kThreads = kWorkers + 64;  // + QK issuer, PV issuer
 constexpr int kTile = 128;             // keys per tile
 constexpr int kHG = 64;                // heads per pass
 constexpr int kPanel = 16384;          // 128 keys x 64 columns bf16
 constexpr int kQChunk = kHG * 128;     // 64 heads x 64 columns bf16
 constexpr int kPBytes = kTile * 128;   // P^T: 128 keys x 64 heads bf16
-constexpr int kSteps = 5;              // runs of four groups (128 columns) of a key (Dk <= 576)
 constexpr int kSCol = 256;             // TMEM: O^T in columns 0..255, S^T behind
 constexpr int kMaxCtas = 148;          // workspace slots (a constant of the sizes alone)
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -77,13 +80,14 @@ struct Params {
 };
 
 struct Shared {
-  uint64_t kfull[4], vfull[4], pvchunk[4], qfull;
+  uint64_t kfull[9], vfull[4], pvchunk[4], qfull;
   uint64_t sfull, pfull, drain[2];
-  uint64_t rv[4], seg;        // the 4 warps of a head quarter meet; all 16 after a segment
-  float mrun[kHG], alpha[kHG], inv[kHG];
-  float red[4][4][16];        // [head quarter][warp][head]
-  int flag[4][2];
-  int scan[16];
+  uint64_t rv[kParts], seg;   // the 4 warps of a part meet; all after a segment
+  alignas(16) float mrun[kHG];  // read as float4
+  float alpha[kHG], inv[kHG];
+  float red[kParts][4][kHP];  // [part][warp][head]
+  int flag[kParts][2];
+  int scan[kWarps];
   int total, seq0, tile0;     // tiles of the batch; this CTA's first sequence and tile in it
   uint32_t tmem_base;
 };
@@ -125,54 +129,79 @@ __device__ __forceinline__ void expand(uint8_t* panel, int row, int half, uint4 
   }
 }
 
-// This thread's share of a tile of one plane: its key's groups hq, hq + 4, ...
-template <int N>
+// This thread's share of a tile of one plane: its key's 64 columns (groups
+// 2 pn, 2 pn + 1) of the panels pn = hh + kParts e, and for keys half of the
+// ninth panel (group 16 + hh, hh < 2).
 struct Codes {
-  uint4 c[N];
-  uint32_t s[N];  // the scale word of groups 4j .. 4j + 3
+  uint4 c[kPE][2], c8;
+  uint32_t s[kPE], s8;  // scale words
 };
-template <int N>
-__device__ __forceinline__ void load_codes(Codes<N>& d, const uint8_t* cache, int width,
-                                           int ps_log2, int page, int slot, int hq) {
+template <bool kKeys>
+__device__ __forceinline__ void load_codes(Codes& d, const uint8_t* cache, int width, int ps_log2,
+                                           int page, int slot, int hh) {
   const int G = kv4::groups(width), ps = 1 << ps_log2;
   const uint8_t* pg = cache + (int64_t)page * kv4::page_bytes(width, ps) + slot * 16;
   const uint8_t* sc = pg + G * ps * 16 - slot * 12;
 #pragma unroll
-  for (int j = 0; j < N; ++j) {
-    d.c[j] = make_uint4(0u, 0u, 0u, 0u);
-    d.s[j] = 0u;
-    if (page >= 0 && 4 * j + hq < G) {
-      d.c[j] = __ldg(reinterpret_cast<const uint4*>(pg + (4 * j + hq) * ps * 16));
-      d.s[j] = __ldg(reinterpret_cast<const uint32_t*>(sc + j * ps * 4));
+  for (int e = 0; e < kPE; ++e) {
+    const int pn = hh + kParts * e;
+    d.c[e][0] = d.c[e][1] = make_uint4(0u, 0u, 0u, 0u);
+    d.s[e] = 0u;
+    if (page >= 0 && 2 * pn < G) {
+      d.c[e][0] = __ldg(reinterpret_cast<const uint4*>(pg + 2 * pn * ps * 16));
+      d.c[e][1] = __ldg(reinterpret_cast<const uint4*>(pg + (2 * pn + 1) * ps * 16));
+      d.s[e] = __ldg(reinterpret_cast<const uint32_t*>(sc + (pn >> 1) * ps * 4));
+    }
+  }
+  if (kKeys) {
+    d.c8 = make_uint4(0u, 0u, 0u, 0u);
+    d.s8 = 0u;
+    if (page >= 0 && G == 18 && hh < 2) {
+      d.c8 = __ldg(reinterpret_cast<const uint4*>(pg + (16 + hh) * ps * 16));
+      d.s8 = __ldg(reinterpret_cast<const uint32_t*>(sc + 4 * ps * 4));
     }
   }
 }
+// Panel hh + kParts e; its groups' scales are half hh & 1 of their word.
+__device__ __forceinline__ void expand_panel(const Codes& d, uint8_t* panels, int r, int e, int hh) {
+  uint8_t* pn = panels + (hh + kParts * e) * kPanel;
+  const uint32_t two = d.s[e] >> (16 * (hh & 1));
+  expand(pn, r, 0, d.c[e][0], two & 0xffu);
+  expand(pn, r, 1, d.c[e][1], (two >> 8) & 0xffu);
+}
 
-// Lane 2h and 2h + 1 receive op over the 32 lanes of v[h].
+// Lanes 4h .. 4h + 3 receive op over the 32 lanes of v[h].
 template <bool kMax>
-__device__ __forceinline__ float reduce16(float (&v)[16]) {
+__device__ __forceinline__ float reduce8(float (&v)[8]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
-  for (int off = 16; off >= 2; off >>= 1) {
+  for (int off = 16; off >= 4; off >>= 1) {
     const bool upper = (lane & off) != 0;
 #pragma unroll
-    for (int j = 0; j < off / 2; ++j) {
-      const float send = upper ? v[j] : v[j + off / 2];
-      const float keep = upper ? v[j + off / 2] : v[j];
+    for (int j = 0; j < off / 4; ++j) {
+      const float send = upper ? v[j] : v[j + off / 4];
+      const float keep = upper ? v[j + off / 4] : v[j];
       const float got = __shfl_xor_sync(0xffffffffu, send, off);
       v[j] = kMax ? fmaxf(keep, got) : keep + got;
     }
   }
-  const float got = __shfl_xor_sync(0xffffffffu, v[0], 1);
-  return kMax ? fmaxf(v[0], got) : v[0] + got;
+#pragma unroll
+  for (int off = 2; off >= 1; off >>= 1) {
+    const float got = __shfl_xor_sync(0xffffffffu, v[0], off);
+    v[0] = kMax ? fmaxf(v[0], got) : v[0] + got;
+  }
+  return v[0];
 }
 
 // Bounded wait of a whole warp: all its lanes go on, or all give up.
 __device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long lim) {
   return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim));
 }
+__device__ __forceinline__ bool warp_spin(uint64_t* bar, uint32_t parity, long long lim) {
+  return __all_sync(0xffffffffu, mbar_wait_spin(bar, parity, lim));
+}
 
-// Warps meet: one arrival per warp (4 of a head quarter, or all 16).
+// Warps meet: one arrival per warp (the 4 of a head half, or all).
 __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& ph, int lane, long long lim) {
   __syncwarp();
   if (lane == 0) mbar_arrive(bar);
@@ -181,8 +210,8 @@ __device__ __forceinline__ bool meet(uint64_t* bar, uint32_t& ph, int lane, long
   return ok;
 }
 
-// One arrival per warp on a barrier of count 16, this warp's shared-memory
-// writes made visible to the tensor cores, and its TMEM accesses done, first.
+// One arrival per warp, this warp's shared-memory writes made visible to the
+// tensor cores, and its TMEM accesses done, first.
 __device__ __forceinline__ void publish(uint64_t* bar, int lane) {
   asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
   tc_fence_before();
@@ -202,28 +231,30 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   uint8_t* const pbuf = p.own_p ? pown : panels + 8 * kPanel;
   Shared* sh = reinterpret_cast<Shared*>(pown + (p.own_p ? kPBytes : 0));
   const Kv4Decode& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int group = blockIdx.x % p.groups, cta = blockIdx.x / p.groups;
   const int h0 = group * kHG, hn = min(kHG, a.num_heads - h0);
   const long long lim = p.wait_ns;
 
   if (tid == 0) {
+    for (int i = 0; i < 9; ++i) mbar_init(&sh->kfull[i], i < 8 ? 4 : 8);
     for (int i = 0; i < 4; ++i) {
-      mbar_init(&sh->kfull[i], 16);
-      mbar_init(&sh->vfull[i], 16);
+      mbar_init(&sh->vfull[i], 8);
       mbar_init(&sh->pvchunk[i], 1);
+    }
+    mbar_init(&sh->drain[0], 1);
+    mbar_init(&sh->drain[1], 1);
+    for (int i = 0; i < kParts; ++i) {
       mbar_init(&sh->rv[i], 4);
       sh->flag[i][0] = sh->flag[i][1] = 0;
     }
     mbar_init(&sh->qfull, 1);
     mbar_init(&sh->sfull, 1);
-    mbar_init(&sh->pfull, 16);
-    mbar_init(&sh->seg, 16);
-    mbar_init(&sh->drain[0], 1);
-    mbar_init(&sh->drain[1], 1);
+    mbar_init(&sh->pfull, kWarps);
+    mbar_init(&sh->seg, kWarps);
     fence_barrier_init();
   }
-  // The sequences' tiles: thread i < 512 owns a run of sequences.
+  // The sequences' tiles: a worker owns a run of sequences.
   const int per = (a.num_seqs + kWorkers - 1) / kWorkers;
   const int b0 = min(a.num_seqs, tid * per), b1 = tid < kWorkers ? min(a.num_seqs, b0 + per) : b0;
   int mine = 0;
@@ -234,15 +265,15 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
     const int v = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += v;
   }
-  if (lane == 31 && warp < 16) sh->scan[warp] = incl;
-  if (warp == 16) tmem_alloc(&sh->tmem_base, 512);
+  if (lane == 31 && warp < kWarps) sh->scan[warp] = incl;
+  if (warp == kWarps) tmem_alloc(&sh->tmem_base, 512);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
   int total = 0;
-  for (int w = 0; w < 16; ++w) {
-    if (w < warp && warp < 16) incl += sh->scan[w];
+  for (int w = 0; w < kWarps; ++w) {
+    if (w < warp && warp < kWarps) incl += sh->scan[w];
     total += sh->scan[w];
   }
   const int g0 = (int)range_start(total, cta, p.ctas), g1 = (int)range_start(total, cta + 1, p.ctas);
@@ -268,10 +299,10 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 
   // Segments of [g0, g1): every role walks them alike.
   int left = g1 - g0, b = left > 0 ? sh->seq0 : 0, ta = left > 0 ? sh->tile0 : 0;
-  if (warp >= 16) {
+  if (warp >= kWarps) {
     // ------------------------------------------------------------ MMA issuers
-    if (lane == 0 && left > 0) {
-      const bool is_pv = warp == 17;
+    if (left > 0) {
+      const bool is_pv = warp == kWarps + 1;
       const int nqk = (hn + 15) & ~15;  // heads of S^T
       const uint32_t id_qk = idesc_bf16_f32(kTile, nqk, false, false);
       constexpr uint32_t id_pv = idesc_bf16_f32(128, kHG, true, true);
@@ -285,57 +316,53 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const int tb = min(tiles_of(seq_keys(a, b).n), ta + left);
         for (int i = ta; i < tb && ok; ++i, ph ^= 1) {
           if (!is_pv) {
-            if (i == ta && !mbar_wait_spin(&sh->qfull, qph, lim)) { ok = false; break; }
+            if (i == ta && !warp_spin(&sh->qfull, qph, lim)) { ok = false; break; }
             for (int c = 0; c < p.nck; ++c) {
-              // step j brought panels 2j, 2j + 1; the last one the ninth, too
-              if (!(c & 1) && c < 8) {
-                if (!mbar_wait_spin(&sh->kfull[c >> 1], ph, lim)) { ok = false; break; }
-                tc_fence_after();
-              }
+              if (!warp_spin(&sh->kfull[c], ph, lim)) { ok = false; break; }
+              tc_fence_after();
               const uint64_t ka = k_desc + (uint64_t)((c * kPanel) >> 4);
               const uint64_t qa = q_desc + (uint64_t)((c * kQChunk) >> 4);
 #pragma unroll
               for (int k = 0; k < 4; ++k)
-                umma_ss(tmem + kSCol, ka + 2 * k, qa + 2 * k, id_qk, (c > 0 || k > 0) ? 1u : 0u);
+                umma_ss_warp(tmem + kSCol, ka + 2 * k, qa + 2 * k, id_qk,
+                             (c > 0 || k > 0) ? 1u : 0u);
             }
-            if (ok) umma_commit(&sh->sfull);
+            if (ok) umma_commit_warp(&sh->sfull);
           } else {
-            if (!mbar_wait_spin(&sh->pfull, ph, lim)) { ok = false; break; }
+            if (!warp_spin(&sh->pfull, ph, lim)) { ok = false; break; }
             tc_fence_after();
             for (int c = 0; c < p.nvc; ++c) {
               if (!kAlias) {
-                if (!mbar_wait_spin(&sh->vfull[c], ph, lim)) { ok = false; break; }
+                if (!warp_spin(&sh->vfull[c], ph, lim)) { ok = false; break; }
                 tc_fence_after();
               }
               const uint64_t va = v_desc + (uint64_t)((2 * c * kPanel) >> 4);
 #pragma unroll
               for (int k = 0; k < 8; ++k)
-                umma_ss(tmem + c * kHG, va + (uint64_t)(k * 128), p_desc + (uint64_t)(k * 128),
-                        id_pv, (i > ta || k > 0) ? 1u : 0u);
-              umma_commit(&sh->pvchunk[c]);
+                umma_ss_warp(tmem + c * kHG, va + (uint64_t)(k * 128), p_desc + (uint64_t)(k * 128),
+                             id_pv, (i > ta || k > 0) ? 1u : 0u);
+              umma_commit_warp(&sh->pvchunk[c]);
             }
           }
         }
         if (tb > ta) qph ^= 1;
         left -= tb - ta;
       }
-      if (!ok) record_status(a.status, HS_ERR_TIMEOUT);
-      umma_commit(&sh->drain[is_pv]);  // every MMA done before TMEM is released
-      mbar_wait(&sh->drain[is_pv], 0, kDefaultWaitNs);
+      if (!ok && lane == 0) record_status(a.status, HS_ERR_TIMEOUT);
+      umma_commit_warp(&sh->drain[is_pv]);  // every MMA done before TMEM is released
+      (void)warp_spin(&sh->drain[is_pv], 0, kDefaultWaitNs);
     }
   } else {
     // ------------------------------------------------------------ expansion, softmax, epilogue
-    const int g4 = warp & 3, hq = warp >> 2;  // TMEM lane quarter, head quarter
+    const int g4 = warp & 3, hh = warp >> 2;  // TMEM lane quarter, part
     const int r = 32 * g4 + lane;             // key row of a tile; row of an O^T chunk
-    const int hb = 16 * hq;
-    const bool act = hb < hn;                 // this quarter has heads
+    const int hb = kHP * hh;
+    const bool act = hb < hn;                 // this part has heads
     const uint32_t lane_base = tmem + ((uint32_t)(32 * g4) << 16);
     const float sl2 = p.scale_log2;
     uint32_t ph = 0, rvph = 0, segph = 0;     // tile parity; parities of the meetings
     bool ok = true, any_pv = false, first_seg = true;
-    Codes<kSteps> kc;
-    Codes<4> vc;
-    int slot = 0;
+    Codes kc;
     // The table entry of this thread's key of a tile, loaded a tile ahead and
     // checked where it is used.
     auto entry_at = [&](const kv4::KeyList& kl, int bb, int tile) -> int {
@@ -344,13 +371,13 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
       const int e = kl.pos(x) >> a.ps_log2;
       return e < a.table_width ? __ldg(a.table + (int64_t)bb * a.table_stride + e) : -1;
     };
-    auto load_k = [&](const kv4::KeyList& kl, int tile, int& page) {
-      if ((unsigned)page >= (unsigned)a.num_pages) {
-        if (tile * kTile + r < kl.n) record_status(a.status, HS_ERR_INVALID_INDEX);
-        page = -1;
-      }
-      slot = kl.pos(tile * kTile + r) & ((1 << a.ps_log2) - 1);
-      load_codes(kc, a.k_cache, a.dk, a.ps_log2, page, slot, hq);
+    auto checked = [&](const kv4::KeyList& kl, int tile, int page) -> int {
+      if ((unsigned)page < (unsigned)a.num_pages) return page;
+      if (tile * kTile + r < kl.n) record_status(a.status, HS_ERR_INVALID_INDEX);
+      return -1;
+    };
+    auto slot_of = [&](const kv4::KeyList& kl, int tile) {
+      return kl.pos(tile * kTile + r) & ((1 << a.ps_log2) - 1);
     };
     for (; left > 0 && ok; ++b, ta = 0) {
       const kv4::KeyList kl = seq_keys(a, b);
@@ -362,55 +389,55 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           tma_load_3d(qbuf + c * kQChunk, &qmap, &sh->qfull, c * 64, h0, b);
       }
       int page = entry_at(kl, b, ta), next = ta + 1 < tb ? entry_at(kl, b, ta + 1) : -1;
-      load_k(kl, ta, page);
-      if (!kAlias) load_codes(vc, a.v_cache, a.dv, a.ps_log2, page, slot, hq);
-      float lpart[16];
+      page = checked(kl, ta, page);
+      load_codes<true>(kc, a.k_cache, a.dk, a.ps_log2, page, slot_of(kl, ta), hh);
+      float lpart[kHP];
 #pragma unroll
-      for (int k = 0; k < 16; ++k) lpart[k] = 0.f;
+      for (int k = 0; k < kHP; ++k) lpart[k] = 0.f;
       for (int i = ta; i < tb && ok; ++i) {
-        // ---- K panels 2j, 2j + 1 of this tile, once PV of the tile before
-        // has read them (and P^T, for the ninth)
+        // ---- this part's K panels, each once PV of the tile before has read it
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          if (2 * j >= p.nck) break;
-          const int c = min(j, p.nvc - 1);
+        for (int e = 0; e < kPE; ++e) {
+          const int pn = hh + kParts * e;
+          if (pn >= p.nck) break;
+          const int c = min(pn >> 1, p.nvc - 1);
           if (any_pv && !warp_wait(&sh->pvchunk[c], ph ^ 1, lim)) { ok = false; break; }
-          const int g = 4 * j + hq;
-          if (g < 2 * p.nck)
-            expand(panels + (g >> 1) * kPanel, r, g & 1, kc.c[j], (kc.s[j] >> (8 * hq)) & 0xffu);
-          if (j == 3 && p.nck == 9) {
-            if (any_pv && !warp_wait(&sh->pvchunk[p.nvc - 1], ph ^ 1, lim)) { ok = false; break; }
-            if (hq < 2)
-              expand(panels + 8 * kPanel, r, hq, kc.c[4], (kc.s[4] >> (8 * hq)) & 0xffu);
-          }
-          publish(&sh->kfull[j], lane);
+          expand_panel(kc, panels, r, e, hh);
+          publish(&sh->kfull[pn], lane);
         }
         if (!ok) break;
-        // the next tile's codes, the table entry of the one after
-        if (i + 1 < tb) {
-          page = next;
-          next = i + 2 < tb ? entry_at(kl, b, i + 2) : -1;
-          load_k(kl, i + 1, page);
+        if (p.nck == 9 && hh < 2) {  // half of the ninth panel, where P^T was
+          if (any_pv && !warp_wait(&sh->pvchunk[p.nvc - 1], ph ^ 1, lim)) { ok = false; break; }
+          expand(panels + 8 * kPanel, r, hh, kc.c8, (kc.s8 >> (8 * hh)) & 0xffu);
+          publish(&sh->kfull[8], lane);
         }
-        // ---- softmax: row r of S^T, heads hb .. hb + 15
+        // ---- codes ahead: the next tile's keys, or this tile's values
+        if (!kAlias) {
+          load_codes<false>(kc, a.v_cache, a.dv, a.ps_log2, page, slot_of(kl, i), hh);
+        } else if (i + 1 < tb) {
+          page = checked(kl, i + 1, next);
+          load_codes<true>(kc, a.k_cache, a.dk, a.ps_log2, page, slot_of(kl, i + 1), hh);
+          if (i + 2 < tb) next = entry_at(kl, b, i + 2);
+        }
+        // ---- softmax: row r of S^T, heads hb .. hb + kHP - 1
         if (!warp_wait(&sh->sfull, ph, lim)) { ok = false; break; }
         // PV of the tile before has read P^T (and V) and added to O^T
         if (any_pv && !warp_wait(&sh->pvchunk[p.nvc - 1], ph ^ 1, lim)) { ok = false; break; }
         tc_fence_after();
         const bool first = i == ta;
         if (act) {
-          uint32_t u[16];
-          tmem_ld16(lane_base + kSCol + hb, u);
+          uint32_t u[kHP];
+          tmem_ld32(lane_base + kSCol + hb, u);
           tmem_ld_wait();
           reg_fence(u);
           const bool valid = i * kTile + r < kl.n;
           const float4* const mr = reinterpret_cast<const float4*>(sh->mrun + hb);
-          float x[16];
+          float x[kHP];
           float most = -INFINITY;  // above the running maximum
 #pragma unroll
-          for (int k = 0; k < 16; ++k) x[k] = valid ? __uint_as_float(u[k]) * sl2 : -INFINITY;
+          for (int k = 0; k < kHP; ++k) x[k] = valid ? __uint_as_float(u[k]) * sl2 : -INFINITY;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+          for (int k = 0; k < kHP / 4; ++k) {
             const float4 m = mr[k];
             most = fmaxf(most, fmaxf(fmaxf(x[4 * k] - m.x, x[4 * k + 1] - m.y),
                                      fmaxf(x[4 * k + 2] - m.z, x[4 * k + 3] - m.w)));
@@ -418,38 +445,61 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
           bool over = first || most > kRescaleLog2;
           const int par = i & 1;
           if (!first) {
-            if (__any_sync(0xffffffffu, over) && lane == 0) sh->flag[hq][par] = 1;
-            if (g4 == 0 && lane == 0) sh->flag[hq][par ^ 1] = 0;
-            if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
-            over = *reinterpret_cast<volatile int*>(&sh->flag[hq][par]) != 0;
+            if (__any_sync(0xffffffffu, over) && lane == 0) sh->flag[hh][par] = 1;
+            if (g4 == 0 && lane == 0) sh->flag[hh][par ^ 1] = 0;
+            if (!meet(&sh->rv[hh], rvph, lane, lim)) { ok = false; break; }
+            over = *reinterpret_cast<volatile int*>(&sh->flag[hh][par]) != 0;
           } else if (g4 == 0 && lane == 0) {
-            sh->flag[hq][0] = sh->flag[hq][1] = 0;  // read next after two rendezvous
+            sh->flag[hh][0] = sh->flag[hh][1] = 0;  // read next after two meetings
           }
-          if (over) {  // the tile's maximum per head joins the running one
-            float y[16];
+          if (over) {
+            // the tile's maximum per head joins the running one (from TMEM
+            // again, 8 heads at a time: rare, and small in code and registers)
+#pragma unroll 1
+            for (int k = 0; k < kHP; k += 8) {
+              uint32_t w[8];
+              tmem_ld8(lane_base + kSCol + hb + k, w);
+              tmem_ld_wait();
+              reg_fence(w);
+              float y[8];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] = x[k];
-            const float wm = reduce16<true>(y);
-            if (!(lane & 1)) sh->red[hq][g4][lane >> 1] = wm;
-            if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
-            if (g4 == 0 && lane < 16) {
-              const float tm = fmaxf(fmaxf(sh->red[hq][0][lane], sh->red[hq][1][lane]),
-                                     fmaxf(sh->red[hq][2][lane], sh->red[hq][3][lane]));
+              for (int e = 0; e < 8; ++e) y[e] = valid ? __uint_as_float(w[e]) * sl2 : -INFINITY;
+              const float wm = reduce8<true>(y);
+              if (!(lane & 3)) sh->red[hh][g4][k + (lane >> 2)] = wm;
+            }
+            if (!meet(&sh->rv[hh], rvph, lane, lim)) { ok = false; break; }
+            if (g4 == 0 && lane < kHP) {
+              const float tm = fmaxf(fmaxf(sh->red[hh][0][lane], sh->red[hh][1][lane]),
+                                     fmaxf(sh->red[hh][2][lane], sh->red[hh][3][lane]));
               const float mo = first ? -INFINITY : sh->mrun[hb + lane];
               const float mn = first || tm > mo + kRescaleLog2 ? tm : mo;
               sh->alpha[hb + lane] = first || mn == mo ? 1.f : fast_exp2(mo - mn);
               sh->mrun[hb + lane] = mn;
             }
-            if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
-          }
-          uint32_t pk[8];
-          const bool resc = over && !first;
-          if (resc) {
+            if (!meet(&sh->rv[hh], rvph, lane, lim)) { ok = false; break; }
+            if (!first) {
 #pragma unroll
-            for (int k = 0; k < 16; ++k) lpart[k] *= sh->alpha[hb + k];
-          }
+              for (int k = 0; k < kHP; ++k) lpart[k] *= sh->alpha[hb + k];
+#pragma unroll 1
+              for (int c = 0; c < p.nvc * (kHP / 8); ++c) {
+                const int k = 8 * (c % (kHP / 8));
+                const uint32_t at = lane_base + (c / (kHP / 8)) * kHG + hb + k;
+                uint32_t w[8];
+                tmem_ld8(at, w);
+                tmem_ld_wait();
+                reg_fence(w);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
+                for (int e = 0; e < 8; ++e)
+                  w[e] = __float_as_uint(__uint_as_float(w[e]) * sh->alpha[hb + k + e]);
+                tmem_st8(at, w);
+              }
+              tmem_st_wait();
+            }
+          }
+          uint8_t* prow = pbuf + r * 128;
+          uint32_t pk[4];
+#pragma unroll
+          for (int k = 0; k < kHP / 4; ++k) {
             // every logit so far -inf: exp2(-inf - 0) = 0
             float4 m = mr[k];
             m.x = m.x == -INFINITY ? 0.f : m.x;
@@ -463,42 +513,28 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             lpart[4 * k + 2] += e2;
             lpart[4 * k + 3] += e3;
             __nv_bfloat162 p0 = __floats2bfloat162_rn(e0, e1), p1 = __floats2bfloat162_rn(e2, e3);
-            pk[2 * k] = *reinterpret_cast<uint32_t*>(&p0);
-            pk[2 * k + 1] = *reinterpret_cast<uint32_t*>(&p1);
+            pk[2 * (k & 1)] = *reinterpret_cast<uint32_t*>(&p0);
+            pk[2 * (k & 1) + 1] = *reinterpret_cast<uint32_t*>(&p1);
+            if (k & 1)
+              *reinterpret_cast<uint4*>(prow + (((kHP / 8 * hh + (k >> 1)) ^ (r & 7)) << 4)) =
+                  make_uint4(pk[0], pk[1], pk[2], pk[3]);
           }
-          if (resc) {
-#pragma unroll 1
-            for (int c = 0; c < p.nvc; ++c) {
-              uint32_t w[16];
-              tmem_ld16(lane_base + c * kHG + hb, w);
-              tmem_ld_wait();
-              reg_fence(w);
-#pragma unroll
-              for (int k = 0; k < 16; ++k)
-                w[k] = __float_as_uint(__uint_as_float(w[k]) * sh->alpha[hb + k]);
-              tmem_st16(lane_base + c * kHG + hb, w);
-            }
-            tmem_st_wait();
-          }
-          uint8_t* prow = pbuf + r * 128;
-          *reinterpret_cast<uint4*>(prow + (((2 * hq) ^ (r & 7)) << 4)) =
-              make_uint4(pk[0], pk[1], pk[2], pk[3]);
-          *reinterpret_cast<uint4*>(prow + (((2 * hq + 1) ^ (r & 7)) << 4)) =
-              make_uint4(pk[4], pk[5], pk[6], pk[7]);
         }
         publish(&sh->pfull, lane);
-        // ---- the value plane's panels (QK has read the keys there)
         if (!kAlias) {
+          // ---- the value plane's panels (QK has read the keys there)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            if (c >= p.nvc) break;
-            const int g = 4 * c + hq;
-            if (g < 2 * p.nvp)
-              expand(panels + (g >> 1) * kPanel, r, g & 1, vc.c[c],
-                     (vc.s[c] >> (8 * hq)) & 0xffu);
-            publish(&sh->vfull[c], lane);
+          for (int e = 0; e < kPE; ++e) {
+            const int pn = hh + kParts * e;
+            if (pn >= 2 * p.nvc) break;
+            if (pn < p.nvp) expand_panel(kc, panels, r, e, hh);
+            publish(&sh->vfull[pn >> 1], lane);
           }
-          if (i + 1 < tb) load_codes(vc, a.v_cache, a.dv, a.ps_log2, page, slot, hq);
+          if (i + 1 < tb) {
+            page = checked(kl, i + 1, next);
+            load_codes<true>(kc, a.k_cache, a.dk, a.ps_log2, page, slot_of(kl, i + 1), hh);
+            if (i + 2 < tb) next = entry_at(kl, b, i + 2);
+          }
         }
         any_pv = true;
         ph ^= 1;
@@ -508,13 +544,19 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
       const bool whole = ta == 0 && tb == nt;
       const int64_t slot2 = ((int64_t)group * p.ctas + cta) * 2 + (first_seg ? 0 : 1);
       if (act) {
-        const float ws = reduce16<false>(lpart);
-        if (!(lane & 1)) sh->red[hq][g4][lane >> 1] = ws;
-        if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
+#pragma unroll
+        for (int k = 0; k < kHP; k += 8) {
+          float y[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = lpart[k + e];
+          const float ws = reduce8<false>(y);
+          if (!(lane & 3)) sh->red[hh][g4][k + (lane >> 2)] = ws;
+        }
+        if (!meet(&sh->rv[hh], rvph, lane, lim)) { ok = false; break; }
         const int h = h0 + hb + lane;
-        if (g4 == 0 && lane < 16 && hb + lane < hn) {
-          const float l = (sh->red[hq][0][lane] + sh->red[hq][1][lane]) +
-                          (sh->red[hq][2][lane] + sh->red[hq][3][lane]);
+        if (g4 == 0 && lane < kHP && hb + lane < hn) {
+          const float l = (sh->red[hh][0][lane] + sh->red[hh][1][lane]) +
+                          (sh->red[hh][2][lane] + sh->red[hh][3][lane]);
           const float m = sh->mrun[hb + lane];
           if (whole) {
             const float sk = a.sink ? __ldg(a.sink + h) * kLog2e : -INFINITY;
@@ -528,34 +570,31 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
             p.part_ml[slot2 * kHG + hb + lane] = make_float2(m, l);
           }
         }
-        if (!meet(&sh->rv[hq], rvph, lane, lim)) { ok = false; break; }
+        if (!meet(&sh->rv[hh], rvph, lane, lim)) { ok = false; break; }
         if (!warp_wait(&sh->pvchunk[p.nvc - 1], ph ^ 1, lim)) { ok = false; break; }
         tc_fence_after();
-        // rows of a chunk = consecutive d: a warp stores 32 of one head at a
-        // time.  Rolled up on purpose: code that runs once per sequence costs
-        // its instruction fetches.
-        const int hc = min(16, hn - hb);
+        // rows of a chunk = consecutive d: a warp stores 32 of one head at a time
+        const int hc = min(kHP, hn - hb);
         __nv_bfloat16* const ob = static_cast<__nv_bfloat16*>(a.out) +
-                                  ((int64_t)b * a.num_heads + h0 + hb) * a.dv;
-        float* const op = p.part_o + (slot2 * kHG + hb) * a.dv;
+                                  ((int64_t)b * a.num_heads + h0 + hb) * a.dv + r;
+        float* const op = p.part_o + (slot2 * kHG + hb) * a.dv + r;
 #pragma unroll 1
         for (int c = 0; c < p.nvc; ++c) {
-          const int d = c * 128 + r;
-#pragma unroll 1
-          for (int k = 0; k < hc; k += 8) {
-            uint32_t w[8];
-            tmem_ld8(lane_base + c * kHG + hb + k, w);
-            tmem_ld_wait();
-            reg_fence(w);
+          uint32_t w[kHP];
+          tmem_ld32(lane_base + c * kHG + hb, w);
+          tmem_ld_wait();
+          reg_fence(w);
+          if (c * 128 + r >= a.dv) continue;
+          if (whole) {
+            __nv_bfloat16* o = ob + c * 128;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              if (d >= a.dv || k + e >= hc) continue;
-              const float v = __uint_as_float(w[e]);
-              if (whole)
-                ob[(k + e) * a.dv + d] = __float2bfloat16_rn(v * sh->inv[hb + k + e]);
-              else
-                op[(k + e) * a.dv + d] = v;
-            }
+            for (int k = 0; k < kHP; ++k, o += a.dv)
+              if (k < hc) *o = __float2bfloat16_rn(__uint_as_float(w[k]) * sh->inv[hb + k]);
+          } else {
+            float* o = op + c * 128;
+#pragma unroll
+            for (int k = 0; k < kHP; ++k, o += a.dv)
+              if (k < hc) *o = __uint_as_float(w[k]);
           }
         }
         tc_fence_before();  // the next segment's first PV follows this thread's P^T
@@ -570,7 +609,7 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 16) tmem_dealloc(tmem, 512);
+  if (warp == kWarps) tmem_dealloc(tmem, 512);
 }
 
 // Joins the partials of a sequence that several CTAs share, and serves empty
