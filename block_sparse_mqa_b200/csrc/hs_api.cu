@@ -208,6 +208,9 @@ int hs_path(int op, hs_dtype dtype, int num_heads, int dk, int dv, int block_siz
         return HS_PATH_TCGEN05;
       return HS_PATH_SIMT;
     case HS_OP_SWA_FIRST_MQA:
+      return !g_force_simt.load() && hs::tc_first_shape_ok(dtype, num_heads, dk, dv)
+                 ? HS_PATH_TCGEN05
+                 : HS_PATH_SIMT;
     case HS_OP_SWA_FIRST_MQA_BWD: return HS_PATH_SIMT;
     case HS_OP_KV4_MQA_DECODE:
       return !g_force_simt.load() && hs::tc_kv4_decode_shape_ok(num_heads, dk, dv, dtype)
@@ -373,7 +376,15 @@ static hs_status attention_common(hs::AttnArgs& a, bool sparse, const void* q, i
   if (total_tokens == 0) return HS_OK;
   r = status_ptr(&a.p.status);
   if (r != HS_OK) return r;
-  const bool tc = dtype == HS_BF16 && !g_force_simt.load() && !a.with_first &&
+  if (a.with_first) {
+    if (!g_force_simt.load() && hs::tc_first_eligible(a.p) &&
+        (reinterpret_cast<uintptr_t>(out) & 15) == 0)
+      return launched_on(hs::launch_tc_first_fwd(a, g_wait_limit.load(), stream),
+                         "tc window attention with first tokens", HS_PATH_TCGEN05);
+    return launched_on(hs::launch_simt_attention(a, false, stream),
+                       "simt window attention with first tokens", HS_PATH_SIMT);
+  }
+  const bool tc = dtype == HS_BF16 && !g_force_simt.load() &&
                   hs::tc_attention_supported(num_heads, dk, dv, a.block_size, sparse) &&
                   hs::tc_attention_eligible(a);
   if (tc) return launched_on(hs::launch_tc_attention(a, sparse, g_wait_limit.load(), stream),

@@ -93,6 +93,12 @@ cudaError_t launch_select_topk(const float* block_score, int nb_stride, const in
                                int num_docs, int total_tokens, int max_seqlen, int block_size,
                                int topk, int32_t* idx, int* status, cudaStream_t s);
 cudaError_t launch_simt_attention(const AttnArgs& a, bool sparse, cudaStream_t s);
+// The window attention's bf16 rows whose lse is NaN, computed again.
+cudaError_t launch_simt_redo(const AttnArgs& a, cudaStream_t s);
+// The window attention with visible first tokens on pairs of CTAs.
+bool tc_first_shape_ok(hs_dtype dtype, int num_heads, int dk, int dv);
+bool tc_first_eligible(const Problem& p);
+cudaError_t launch_tc_first_fwd(const AttnArgs& a, long long wait_limit, cudaStream_t s);
 size_t simt_backward_workspace(int total_tokens, int num_heads);
 // *path (may be null) receives the kernel family the dq and dk / dv passes use.
 cudaError_t launch_simt_backward(const BwdArgs& a, bool sparse, bool allow_mma, int* path,

@@ -136,17 +136,13 @@ __device__ __forceinline__ float block_reduce_sum(float v, float* red) {
   return r;
 }
 
-// One CTA per (query token, head).  Keys come in segments of at most 128
+// One (query token, head) by one CTA.  Keys come in segments of at most 128
 // (one selected block, or one slice of the window); an online softmax keeps
 // the running max m, the running denominator l and the output accumulators
 // (thread i owns value columns i, i + 128, ...).  The sink joins at the end.
 template <typename T, bool kSparse>
-__global__ void __launch_bounds__(kAttnThreads)
-simt_attention_kernel(AttnArgs a) {
-  extern __shared__ float smem[];
+__device__ __forceinline__ void attend_row(const AttnArgs& a, int t, int h, float* smem) {
   const Problem& p = a.p;
-  const int t = blockIdx.x, h = blockIdx.y;
-  if (t >= p.total_tokens || h >= p.num_heads) return;
   int bos, eos;
   if (!find_doc(p.cu_seqlens, p.num_docs, p.total_tokens, p.max_seqlen, t, bos, eos, p.status))
     return;
@@ -250,6 +246,38 @@ simt_attention_kernel(AttnArgs a) {
   if (tid == 0) a.lse[(int64_t)t * p.num_heads + h] = lse;
 }
 
+template <typename T, bool kSparse>
+__global__ void __launch_bounds__(kAttnThreads)
+simt_attention_kernel(AttnArgs a) {
+  extern __shared__ float smem[];
+  const int t = blockIdx.x, h = blockIdx.y;
+  if (t >= a.p.total_tokens || h >= a.p.num_heads) return;
+  attend_row<T, kSparse>(a, t, h, smem);
+}
+
+// The rows whose lse is NaN, again: a tensor-core kernel reads whole tiles, and
+// a value outside the key set that is not finite makes a result NaN.  Without
+// such rows this reads lse once.
+__global__ void __launch_bounds__(kAttnThreads) simt_redo_kernel(AttnArgs a) {
+  extern __shared__ float smem[];
+  __shared__ int marked[kAttnThreads];
+  const int64_t n = (int64_t)a.p.total_tokens * a.p.num_heads;
+  for (int64_t base = (int64_t)blockIdx.x * kAttnThreads; base < n;
+       base += (int64_t)gridDim.x * kAttnThreads) {
+    const int64_t th = base + threadIdx.x;
+    const int mark = th < n && isnan(a.lse[th]);
+    marked[threadIdx.x] = mark;
+    if (!__syncthreads_or(mark)) continue;
+    for (int i = 0; i < kAttnThreads; ++i) {
+      if (!marked[i]) continue;
+      attend_row<__nv_bfloat16, false>(a, (int)((base + i) / a.p.num_heads),
+                                       (int)((base + i) % a.p.num_heads), smem);
+      __syncthreads();
+    }
+    __syncthreads();
+  }
+}
+
 }  // namespace
 
 size_t simt_block_score_smem(int num_heads, int dk, int nbmax) {
@@ -269,6 +297,14 @@ cudaError_t launch_simt_block_score(const ScoreArgs& a, cudaStream_t s) {
     if (e != cudaSuccess) return e;
     kern<<<a.p.total_tokens, kScoreThreads, smem, s>>>(a);
   }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_simt_redo(const AttnArgs& a, cudaStream_t s) {
+  if (a.p.dv > kAttnThreads * kMaxDvPerThread) return cudaErrorInvalidValue;
+  const int64_t blocks = ((int64_t)a.p.total_tokens * a.p.num_heads + kAttnThreads - 1) / kAttnThreads;
+  const size_t smem = sizeof(float) * ((size_t)a.p.dk + 128 + 32);
+  simt_redo_kernel<<<(unsigned)(blocks < 592 ? blocks : 592), kAttnThreads, smem, s>>>(a);
   return cudaGetLastError();
 }
 
