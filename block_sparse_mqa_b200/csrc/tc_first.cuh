@@ -24,11 +24,21 @@ struct Docs {
   int window, first;
 };
 
+__device__ __forceinline__ uint32_t low_bits(int n) {  // the lowest n, n >= 1
+  return n >= 32 ? 0xffffffffu : (1u << n) - 1u;
+}
+// Bits lo .. hi (clipped to 0 .. 31).
+__device__ __forceinline__ uint32_t range_bits(int lo, int hi) {
+  if (hi < 0 || lo > 31 || lo > hi) return 0u;
+  return (lo <= 0 ? 0xffffffffu : 0xffffffffu << lo) & low_bits(hi + 1);
+}
+
 // Slots a token sees: lo .. hi of the window's and f0 .. f0 + nf - 1.
 struct Mask {
   int lo, hi, f0, nf;
-  __device__ __forceinline__ bool sees(int s) const {
-    return (unsigned)(s - lo) <= (unsigned)(hi - lo) || (unsigned)(s - f0) < (unsigned)nf;
+  // of the 32 slots from s
+  __device__ __forceinline__ uint32_t bits(int s) const {
+    return range_bits(lo - s, hi - s) | range_bits(f0 - s, f0 + nf - 1 - s);
   }
 };
 

@@ -31,7 +31,6 @@
 // softmax of tile i.  The running maximum is raised only past 2^8.
 // All waits are bounded (HS_ERR_TIMEOUT).
 
-#include <float.h>
 #include <math.h>
 
 #include "hs_device.cuh"
@@ -147,7 +146,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     bool first_pass = true;
     // a free slot, armed by the leader for both CTAs' bytes
     auto claim = [&](int bytes) -> bool {
-      if (!warp_wait_cluster(&emptyb[slot], ph ^ 1, lim)) return false;
+      if (!warp_wait(&emptyb[slot], ph ^ 1, lim)) return false;
       if (leader && lane == 0) mbar_expect_tx(&fullb[slot], 2 * bytes);
       __syncwarp();
       return true;
@@ -161,7 +160,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     while (ok && walk.next(ps, leader && !is_v ? p.status : nullptr)) {
       if (!is_v) {  // Q chunks, each once the pass before has read it
         for (int c = 0; c < p.nck && ok; ++c) {
-          if (!first_pass && !warp_wait_cluster(&sh->qempty[c], qph ^ 1, lim)) { ok = false; break; }
+          if (!first_pass && !warp_wait(&sh->qempty[c], qph ^ 1, lim)) { ok = false; break; }
           if (lane == 0) {
             if (leader) mbar_expect_tx(&sh->qfull[c], 2 * kQChunk);
             tma_pair_3d(qbuf + c * kQChunk, &qmap, leader_addr(&sh->qfull[c]), c * 64, 0,
@@ -220,11 +219,11 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           if (!is_pv) {
             const uint32_t id = idesc_bf16_f32(128, n, false, false);
             const uint32_t buf = sidx & 1, d = tmem + kSCol + buf * 128;
-            if (!warp_wait_cluster(&sh->sempty[buf], ((sidx >> 1) & 1) ^ 1, lim)) { ok = false; break; }
+            if (!warp_wait(&sh->sempty[buf], ((sidx >> 1) & 1) ^ 1, lim)) { ok = false; break; }
             tc_fence_after();
             for (int c = 0; c < p.nck; ++c) {
-              if (!warp_wait_cluster(&sh->kfull[slot], ph, lim) ||
-                  (i == 0 && !warp_wait_cluster(&sh->qfull[c], npass & 1, lim))) {
+              if (!warp_wait(&sh->kfull[slot], ph, lim) ||
+                  (i == 0 && !warp_wait(&sh->qfull[c], npass & 1, lim))) {
                 ok = false;
                 break;
               }
@@ -245,8 +244,8 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             commit_pair(&sh->sfull[buf]);
             ++sidx;
           } else {
-            if (!warp_wait_cluster(&sh->pfull, npv & 1, lim) ||
-                (i == 0 && npass > 0 && !warp_wait_cluster(&sh->oempty, (npass - 1) & 1, lim))) {
+            if (!warp_wait(&sh->pfull, npv & 1, lim) ||
+                (i == 0 && npass > 0 && !warp_wait(&sh->oempty, (npass - 1) & 1, lim))) {
               ok = false;
               break;
             }
@@ -254,7 +253,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             for (int b = 0; b < p.nvb && ok; b += 2) {
               const uint32_t id = idesc_bf16_f32(128, b + 1 < p.nvb ? 256 : 128, false, true);
               for (int k0 = 0; k0 < n; k0 += 128) {
-                if (!warp_wait_cluster(&sh->vfull[slot], ph, lim)) { ok = false; break; }
+                if (!warp_wait(&sh->vfull[slot], ph, lim)) { ok = false; break; }
                 tc_fence_after();
                 const uint64_t v = v_desc + (uint64_t)((slot * kVSlot) >> 4);
                 const uint64_t a = p_desc + (uint64_t)(((k0 >> 6) * kPPanel) >> 4);
@@ -285,7 +284,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       }
       if (!ok && lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
       commit_pair(&sh->drain[is_pv]);  // every MMA done before TMEM is released
-      (void)warp_wait_cluster(&sh->drain[is_pv], 0, kDefaultWaitNs);
+      (void)warp_wait(&sh->drain[is_pv], 0, kDefaultWaitNs);
     }
   } else {
     // ------------------------------------------------------------ softmax + epilogue
@@ -299,7 +298,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     auto meet = [&]() -> bool {  // the 8 warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->rv);
-      const bool good = __all_sync(0xffffffffu, mbar_wait(&sh->rv, rvph, lim));
+      const bool good = warp_wait(&sh->rv, rvph, lim);
       rvph ^= 1;
       return good;
     };
@@ -310,7 +309,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     };
     // PV of the tile before has read P and added to O
     auto pv_before = [&]() -> bool {
-      return npv == 0 || __all_sync(0xffffffffu, mbar_wait(&sh->pvdone, (npv - 1) & 1, lim));
+      return npv == 0 || warp_wait(&sh->pvdone, (npv - 1) & 1, lim);
     };
     while (ok && walk.next(ps, nullptr)) {
       const bool act = ps.active(rank);
@@ -320,37 +319,48 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         const int n2 = ps.keys(i) / 2;  // columns of a lane half
         const int col0 = 64 * ch;
         const uint32_t buf = sidx & 1;
-        if (!__all_sync(0xffffffffu, mbar_wait(&sh->sfull[buf], (sidx >> 1) & 1, lim))) {
+        if (!warp_wait(&sh->sfull[buf], (sidx >> 1) & 1, lim)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        float x[64];
-        if (act && col0 < n2) {
-          uint32_t u[32];
+        // x: raw scores (scale joins in the exponential's fma)
+        float x[2][32];
+        float mx = -INFINITY;
+        const int slot0 = 256 * i + hi * n2 + col0;  // of x[0][0]
+        if (act) {
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
+            if (col0 + 32 * e >= n2) break;
+            uint32_t u[32];
             tmem_ld32(lane_base + kSCol + buf * 128 + col0 + 32 * e, u);
             tmem_ld_wait();
             reg_fence(u);
 #pragma unroll
-            for (int k = 0; k < 32; ++k) x[32 * e + k] = __uint_as_float(u[k]) * sl2;
+            for (int k = 0; k < 32; ++k) x[e][k] = __uint_as_float(u[k]);
           }
         }
         ++sidx;
         tell_leader(&sh->sempty[buf]);
-        const int slot0 = 256 * i + hi * n2 + col0;  // of x[0]
-        float mx = -INFINITY;
-        if (act && col0 < n2) {
-          if (!(slot0 >= mk.lo && slot0 + 63 <= mk.hi && col0 + 64 <= n2)) {
-#pragma unroll
-            for (int k = 0; k < 64; ++k)
-              if (!(col0 + k < n2 && mk.sees(slot0 + k))) x[k] = -INFINITY;
-          }
-#pragma unroll
-          for (int k = 0; k < 64; ++k) mx = fmaxf(mx, x[k]);
-        }
         if (act) {
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (col0 + 32 * e >= n2) break;
+            const uint32_t bits =
+                mk.bits(slot0 + 32 * e) & low_bits(n2 - col0 - 32 * e);
+            if (bits != 0xffffffffu) {
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!(bits & (1u << k))) x[e][k] = -INFINITY;
+            }
+            float m4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int k = 0; k < 32; k += 4)
+#pragma unroll
+              for (int j = 0; j < 4; ++j) m4[j] = fmaxf(m4[j], x[e][k + j]);
+            mx = fmaxf(fmaxf(mx, fmaxf(m4[0], m4[1])), fmaxf(m4[2], m4[3]));
+          }
+          mx *= sl2;
           sh->red[i & 1][part][row] = mx;
           if (!meet()) { ok = false; break; }
           const float mt = fmaxf(fmaxf(sh->red[i & 1][0][row], sh->red[i & 1][1][row]),
@@ -359,6 +369,23 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
           m = mn;
           l *= alpha;
+          const float ms = m == -INFINITY ? 0.f : m;  // no key yet: exp2(-inf) = 0
+          uint32_t pk[2][16];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            if (col0 + 32 * e >= n2) break;
+            float la = 0.f, lb = 0.f;
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float e0 = fast_exp2(fmaf(x[e][2 * k], sl2, -ms));
+              const float e1 = fast_exp2(fmaf(x[e][2 * k + 1], sl2, -ms));
+              la += e0;
+              lb += e1;
+              __nv_bfloat162 pr = __floats2bfloat162_rn(e0, e1);
+              pk[e][k] = *reinterpret_cast<uint32_t*>(&pr);
+            }
+            l += la + lb;
+          }
           if (!pv_before()) { ok = false; break; }
           tc_fence_after();
           if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
@@ -376,26 +403,15 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             }
             tmem_st_wait();
           }
-          if (col0 < n2) {
-            const float ms = m == -INFINITY ? 0.f : m;  // no key yet: exp2(-inf) = 0
-            const int key0 = hi * n2 + col0;
+          const int key0 = hi * n2 + col0;
 #pragma unroll
-            for (int q = 0; q < 8; ++q) {
-              if (col0 + 8 * q >= n2) break;
-              uint32_t w[4];
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float e0 = fast_exp2(x[8 * q + 2 * e] - ms);
-                const float e1 = fast_exp2(x[8 * q + 2 * e + 1] - ms);
-                l += e0 + e1;
-                __nv_bfloat162 pr = __floats2bfloat162_rn(e0, e1);
-                w[e] = *reinterpret_cast<uint32_t*>(&pr);
-              }
-              const int key = key0 + 8 * q;
-              *reinterpret_cast<uint4*>(pbuf + (key >> 6) * kPPanel + row * 128 +
-                                        ((((key >> 3) & 7) ^ (row & 7)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
+          for (int q = 0; q < 8; ++q) {
+            if (col0 + 8 * q >= n2) break;
+            const int key = key0 + 8 * q;
+            const uint32_t* w = pk[q >> 2] + 4 * (q & 3);
+            *reinterpret_cast<uint4*>(pbuf + (key >> 6) * kPPanel + row * 128 +
+                                      ((((key >> 3) & 7) ^ (row & 7)) << 4)) =
+                make_uint4(w[0], w[1], w[2], w[3]);
           }
           asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         } else if (!pv_before()) {  // no arrival for a tile before the last one's is used
@@ -423,11 +439,11 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         inv = den == 0.f ? 0.f : em / den;
         lse = den == 0.f ? -INFINITY : (Ms + fast_log2(den)) * kLn2;
       }
-      if (!__all_sync(0xffffffffu, mbar_wait(&sh->pvdone, (npv - 1) & 1, lim))) { ok = false; break; }
+      if (!warp_wait(&sh->pvdone, (npv - 1) & 1, lim)) { ok = false; break; }
       tc_fence_after();
       if (act) {
         __nv_bfloat16* const o = p.out + ((int64_t)t * kH + row) * p.dv;
-        bool bad = false;
+        float finite = 0.f;
 #pragma unroll 1
         for (int c = 0; c < p.nvb * 64; c += 32) {
           if (((c >> 5) & 1) != ch) continue;
@@ -439,20 +455,21 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
           tmem_ld_wait();
           reg_fence(w);
           if (d >= p.dv) continue;
-          uint32_t v[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) {
-            const float a = __uint_as_float(w[2 * k]) * inv, bq = __uint_as_float(w[2 * k + 1]) * inv;
-            bad = bad || !(fabsf(a) <= FLT_MAX) || !(fabsf(bq) <= FLT_MAX);
-            __nv_bfloat162 pr = __floats2bfloat162_rn(a, bq);
-            v[k] = *reinterpret_cast<uint32_t*>(&pr);
+          for (int q = 0; q < 4; ++q) {
+            uint32_t v[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float a = __uint_as_float(w[8 * q + 2 * k]) * inv;
+              const float c1 = __uint_as_float(w[8 * q + 2 * k + 1]) * inv;
+              finite = fmaf(a, 0.f, fmaf(c1, 0.f, finite));  // NaN from NaN and infinities
+              __nv_bfloat162 pr = __floats2bfloat162_rn(a, c1);
+              v[k] = *reinterpret_cast<uint32_t*>(&pr);
+            }
+            reinterpret_cast<uint4*>(o + d)[q] = make_uint4(v[0], v[1], v[2], v[3]);
           }
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            reinterpret_cast<uint4*>(o + d)[k] =
-                make_uint4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
         }
-        if (bad) sh->bad[row] = 1;
+        if (finite != 0.f) sh->bad[row] = 1;
         tell_leader(&sh->oempty);
         if (!meet()) { ok = false; break; }
         if (part == 0)

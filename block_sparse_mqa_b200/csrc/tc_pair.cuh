@@ -30,37 +30,17 @@ __device__ __forceinline__ uint32_t leader_addr(const void* p) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(a) : "r"(smem_u32(p)));
   return a;
 }
+// An arrival on the leader's copy.  What it announces are this CTA's shared
+// memory (behind a proxy fence) and TMEM (behind a tcgen05 fence), which the
+// leader's MMAs read here, so a cluster-wide release, which waits for every
+// earlier access, is not needed.
 __device__ __forceinline__ void arrive_leader(uint64_t* bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(
-                   leader_addr(bar))
-               : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(leader_addr(bar)) : "memory");
 }
 
-// Bounded wait (see mbar_wait) that also orders the other CTA's arrivals.
-__device__ __forceinline__ bool try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-      "selp.u32 %0, 1, 0, p;\n\t}"
-      : "=r"(ok)
-      : "r"(smem_u32(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-__device__ __forceinline__ bool wait_cluster(uint64_t* bar, uint32_t parity, long long limit_ns) {
-  if (try_wait_cluster(bar, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (try_wait_cluster(bar, parity)) return true;
-    if ((long long)(global_ns() - t0) > limit_ns) return false;
-  }
-}
-// A whole warp waits: all its lanes go on, or all give up.
-__device__ __forceinline__ bool warp_wait_cluster(uint64_t* bar, uint32_t parity, long long lim) {
-  return __all_sync(0xffffffffu, wait_cluster(bar, parity, lim));
+// A whole warp waits (see mbar_wait): all its lanes go on, or all give up.
+__device__ __forceinline__ bool warp_wait(uint64_t* bar, uint32_t parity, long long lim) {
+  return __all_sync(0xffffffffu, mbar_wait(bar, parity, lim));
 }
 
 // TMEM of both CTAs (one warp of each executes these).
