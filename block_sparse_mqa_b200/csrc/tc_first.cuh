@@ -102,20 +102,21 @@ struct Walk {
 };
 
 // `rows` (a multiple of 16) key rows of slots s0 .., `panels` panels of 64
-// columns from col, into a slot: panels of 16 KB, a row's 128 bytes swizzled.
+// columns from col, `pitch` bytes apart; a row's 128 bytes are swizzled.
 // One box where 128 rows are consecutive keys, else boxes of 16 rows spread
 // over the lanes.
 __device__ __forceinline__ void load_rows(const Pass& ps, const CUtensorMap* big,
                                           const CUtensorMap* small, uint8_t* dst, uint32_t bar,
-                                          int s0, int rows, int col, int lane, int panels) {
+                                          int s0, int rows, int col, int lane, int panels,
+                                          int pitch) {
   if (rows == 128 && s0 + 128 <= ps.nwp) {
     if (lane < panels)
-      tc::tma_pair_2d(dst + lane * 16384, big, bar, col + 64 * lane, ps.wlo + s0);
+      tc::tma_pair_2d(dst + lane * pitch, big, bar, col + 64 * lane, ps.wlo + s0);
   } else {
     const int boxes = rows / 16;
     for (int e = lane; e < boxes * panels; e += 32) {
       const int pn = e / boxes, bx = e - pn * boxes;
-      tc::tma_pair_2d(dst + pn * 16384 + bx * 2048, small, bar, col + 64 * pn,
+      tc::tma_pair_2d(dst + pn * pitch + bx * 2048, small, bar, col + 64 * pn,
                       ps.row(s0 + 16 * bx));
     }
   }

@@ -26,9 +26,10 @@
 // row whose result is not finite is marked by a NaN lse and computed again by
 // launch_simt_redo, which reads nothing but the key set.
 //
-// Roles per CTA: K and V producers, 8 softmax warps; in the leader the QK and
-// the PV issuer.  S is double-buffered, so QK of tile i + 1 runs beside the
-// softmax of tile i.  The running maximum is raised only past 2^8.
+// Roles per CTA: K and V producers, 8 softmax warps, 4 epilogue warps; in the
+// leader the QK and the PV issuer.  S is double-buffered, so QK of tile i + 1
+// runs beside the softmax of tile i, and the output of a pass leaves while the
+// next one begins.  The running maximum is raised only past 2^8.
 // All waits are bounded (HS_ERR_TIMEOUT).
 
 #include <math.h>
@@ -45,7 +46,8 @@ namespace {
 using namespace tc;
 using namespace first;
 
-constexpr int kThreads = 384;  // 8 softmax warps, K and V producers, QK and PV issuers
+constexpr int kThreads = 512;  // 8 softmax warps; K and V producers, QK and PV issuers; 4 epilogue warps
+constexpr int kStage = 2048;            // per epilogue warp: 32 rows x 32 columns bf16
 constexpr int kKProd = 8, kVProd = 9, kQkWarp = 10, kPvWarp = 11;
 constexpr int kKSlots = 3, kVSlots = 2;
 constexpr int kKSlot = 16384;           // 128 keys x 64 columns
@@ -72,27 +74,30 @@ struct Params {
 struct Shared {
   uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
   uint64_t qfull[kMaxQC], qempty[kMaxQC];
-  uint64_t sfull[2], sempty[2], pfull, pvdone, oempty, drain[2], rv;
+  uint64_t sfull[2], sempty[2], pfull, pvdone, oempty, drain[2], rv, stat;
   float red[2][4][kH];
-  int bad[kH];
+  float inv[2][kH];  // by pass parity
   uint32_t tmem_base;
 };
-constexpr size_t kSmem = 1024 + (size_t)kKSlots * kKSlot + (size_t)kVSlots * kVSlot +
-                         (size_t)kMaxQC * kQChunk + kPBytes + sizeof(Shared);
+constexpr size_t kSmem = (size_t)kKSlots * kKSlot + (size_t)kVSlots * kVSlot +
+                         (size_t)kMaxQC * kQChunk + kPBytes + 4 * kStage + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap kmap16,
                     const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap vmap16,
                     const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* const kring = base;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];  // no room to align it by hand
+  if (smem_u32(smem_raw) & 1023) {
+    record_status(p.status, HS_ERR_CUDA);
+    return;  // every thread of both CTAs alike
+  }
+  uint8_t* const kring = smem_raw;
   uint8_t* const vring = kring + kKSlots * kKSlot;
   uint8_t* const qbuf = vring + kVSlots * kVSlot;
   uint8_t* const pbuf = qbuf + kMaxQC * kQChunk;
-  Shared* sh = reinterpret_cast<Shared*>(pbuf + kPBytes);
+  uint8_t* const stage = pbuf + kPBytes;
+  Shared* sh = reinterpret_cast<Shared*>(stage + 4 * kStage);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = (int)cluster_rank();
   const bool leader = rank == 0;
@@ -118,8 +123,9 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     }
     mbar_init(&sh->pfull, 16);
     mbar_init(&sh->pvdone, 1);
-    mbar_init(&sh->oempty, 16);
+    mbar_init(&sh->oempty, 8);  // 4 epilogue warps of each CTA
     mbar_init(&sh->rv, 8);
+    mbar_init(&sh->stat, 8);
     fence_barrier_init();
   }
   if (warp == kQkWarp) tmem_alloc_pair(&sh->tmem_base, 512);
@@ -128,173 +134,22 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   cluster_sync();  // barriers of both CTAs exist
   tc_fence_after();
   const uint32_t tmem = sh->tmem_base;
+  // registers: 512 threads launch with 128 each; 8 softmax warps take 168 and
+  // the other two warpgroups give 48 each (8 * 168 + 8 * 80 <= 16 * 128)
   Walk walk(p.d, blockIdx.x >> 1, gridDim.x >> 1);
   Pass ps;
   bool ok = true;
 
-  if (warp == kKProd || warp == kVProd) {
-    // ------------------------------------------------------------ producers
-    const bool is_v = warp == kVProd;
-    uint64_t* const fullb = is_v ? sh->vfull : sh->kfull;
-    uint64_t* const emptyb = is_v ? sh->vempty : sh->kempty;
-    uint8_t* const ring = is_v ? vring : kring;
-    const int slots = is_v ? kVSlots : kKSlots, slot_bytes = is_v ? kVSlot : kKSlot;
-    const CUtensorMap* const big = is_v ? &vmap : &kmap;
-    const CUtensorMap* const small = is_v ? &vmap16 : &kmap16;
-    int slot = 0;
-    uint32_t ph = 0, qph = 0;
-    bool first_pass = true;
-    // a free slot, armed by the leader for both CTAs' bytes
-    auto claim = [&](int bytes) -> bool {
-      if (!warp_wait(&emptyb[slot], ph ^ 1, lim)) return false;
-      if (leader && lane == 0) mbar_expect_tx(&fullb[slot], 2 * bytes);
-      __syncwarp();
-      return true;
-    };
-    auto next = [&]() {
-      if (++slot == slots) {
-        slot = 0;
-        ph ^= 1;
-      }
-    };
-    while (ok && walk.next(ps, leader && !is_v ? p.status : nullptr)) {
-      if (!is_v) {  // Q chunks, each once the pass before has read it
-        for (int c = 0; c < p.nck && ok; ++c) {
-          if (!first_pass && !warp_wait(&sh->qempty[c], qph ^ 1, lim)) { ok = false; break; }
-          if (lane == 0) {
-            if (leader) mbar_expect_tx(&sh->qfull[c], 2 * kQChunk);
-            tma_pair_3d(qbuf + c * kQChunk, &qmap, leader_addr(&sh->qfull[c]), c * 64, 0,
-                        ps.token(rank));
-          }
-          __syncwarp();
-        }
-        first_pass = false;
-        qph ^= 1;
-      }
-      for (int i = 0; i < ps.ntile && ok; ++i) {
-        const int n = ps.keys(i);
-        if (!is_v) {
-          const int s0 = 256 * i + rank * (n / 2), rows = n / 2;
-          for (int c = 0; c < p.nck && ok; ++c, next()) {
-            if (!claim(rows * 128)) { ok = false; break; }
-            load_rows(ps, big, small, ring + slot * slot_bytes, leader_addr(&fullb[slot]), s0, rows,
-                      c * 64, lane, 1);
-          }
-        } else {
-          for (int b = 0; b < p.nvb && ok; b += 2) {
-            // 256 columns: 128 (two panels) of each CTA; a last odd block: 64 of each
-            const int panels = b + 1 < p.nvb ? 2 : 1;
-            const int col = b * 128 + rank * panels * 64;
-            for (int k0 = 0; k0 < n && ok; k0 += 128, next()) {
-              const int rows = min(128, n - k0);
-              if (!claim(rows * 128 * panels)) { ok = false; break; }
-              load_rows(ps, big, small, ring + slot * slot_bytes, leader_addr(&fullb[slot]),
-                        256 * i + k0, rows, col, lane, panels);
-            }
-          }
-        }
-      }
-    }
-    if (!ok) {
-      // The leader's barriers count both CTAs' copies and its issuers wait for
-      // all of them; after a timeout they do not, so copies still under way get
-      // a millisecond to land before the CTA may exit.
-      if (lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
-      for (const uint64_t from = global_ns(); global_ns() - from < 1000000;) {
-      }
-    }
-  } else if (warp == kQkWarp || warp == kPvWarp) {
-    // ------------------------------------------------------------ MMA issuers
-    if (leader) {
-      const bool is_pv = warp == kPvWarp;
-      const uint64_t k_desc = umma_desc_sw128(smem_u32(kring), 16, 1024);
-      const uint64_t q_desc = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
-      const uint64_t v_desc = umma_desc_sw128(smem_u32(vring), 16384, 1024);
-      const uint64_t p_desc = umma_desc_sw128(smem_u32(pbuf), 16, 1024);
-      int slot = 0;
-      uint32_t ph = 0, sidx = 0, npv = 0, npass = 0;
-      while (ok && walk.next(ps, nullptr)) {
-        for (int i = 0; i < ps.ntile && ok; ++i) {
-          const int n = ps.keys(i);
-          if (!is_pv) {
-            const uint32_t id = idesc_bf16_f32(128, n, false, false);
-            const uint32_t buf = sidx & 1, d = tmem + kSCol + buf * 128;
-            if (!warp_wait(&sh->sempty[buf], ((sidx >> 1) & 1) ^ 1, lim)) { ok = false; break; }
-            tc_fence_after();
-            for (int c = 0; c < p.nck; ++c) {
-              if (!warp_wait(&sh->kfull[slot], ph, lim) ||
-                  (i == 0 && !warp_wait(&sh->qfull[c], npass & 1, lim))) {
-                ok = false;
-                break;
-              }
-              tc_fence_after();
-              const uint64_t a = q_desc + (uint64_t)((c * kQChunk) >> 4);
-              const uint64_t b = k_desc + (uint64_t)((slot * kKSlot) >> 4);
-#pragma unroll
-              for (int k = 0; k < 4; ++k)
-                umma_pair(d, a + 2 * k, b + 2 * k, id, (c > 0 || k > 0) ? 1u : 0u);
-              commit_pair(&sh->kempty[slot]);
-              if (i + 1 == ps.ntile) commit_pair(&sh->qempty[c]);
-              if (++slot == kKSlots) {
-                slot = 0;
-                ph ^= 1;
-              }
-            }
-            if (!ok) break;
-            commit_pair(&sh->sfull[buf]);
-            ++sidx;
-          } else {
-            if (!warp_wait(&sh->pfull, npv & 1, lim) ||
-                (i == 0 && npass > 0 && !warp_wait(&sh->oempty, (npass - 1) & 1, lim))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            for (int b = 0; b < p.nvb && ok; b += 2) {
-              const uint32_t id = idesc_bf16_f32(128, b + 1 < p.nvb ? 256 : 128, false, true);
-              for (int k0 = 0; k0 < n; k0 += 128) {
-                if (!warp_wait(&sh->vfull[slot], ph, lim)) { ok = false; break; }
-                tc_fence_after();
-                const uint64_t v = v_desc + (uint64_t)((slot * kVSlot) >> 4);
-                const uint64_t a = p_desc + (uint64_t)(((k0 >> 6) * kPPanel) >> 4);
-                const int steps = min(128, n - k0) / 16;
-                if (steps == 8) {
-#pragma unroll
-                  for (int k = 0; k < 8; ++k)
-                    umma_pair(tmem + b * 64, a + (uint64_t)(((k >> 2) * kPPanel) >> 4) + 2 * (k & 3),
-                              v + (uint64_t)(k * 128), id, (i > 0 || k0 > 0 || k > 0) ? 1u : 0u);
-                } else {
-                  for (int k = 0; k < steps; ++k)
-                    umma_pair(tmem + b * 64, a + (uint64_t)(((k >> 2) * kPPanel) >> 4) + 2 * (k & 3),
-                              v + (uint64_t)(k * 128), id, (i > 0 || k0 > 0 || k > 0) ? 1u : 0u);
-                }
-                commit_pair(&sh->vempty[slot]);
-                if (++slot == kVSlots) {
-                  slot = 0;
-                  ph ^= 1;
-                }
-              }
-            }
-            if (!ok) break;
-            commit_pair(&sh->pvdone);
-            ++npv;
-          }
-        }
-        ++npass;
-      }
-      if (!ok && lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
-      commit_pair(&sh->drain[is_pv]);  // every MMA done before TMEM is released
-      (void)warp_wait(&sh->drain[is_pv], 0, kDefaultWaitNs);
-    }
-  } else {
-    // ------------------------------------------------------------ softmax + epilogue
+  if (warp < 8) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+    // ------------------------------------------------------------ softmax
     // Thread: TMEM lane 32 g4 + lane = (half of the tile's keys, row = head),
     // columns 64 ch .. of that half; part = which of the row's four threads.
     const int g4 = warp & 3, ch = warp >> 2, hi = g4 >> 1, part = 2 * hi + ch;
     const int row = 32 * (g4 & 1) + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * g4) << 16);
     const float sl2 = p.scale_log2;
-    uint32_t sidx = 0, npv = 0, rvph = 0;
+    uint32_t sidx = 0, npv = 0, rvph = 0, npass = 0;
     auto meet = [&]() -> bool {  // the 8 warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->rv);
@@ -422,63 +277,250 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
         tell_leader(&sh->pfull);
       }
       if (!ok) break;
-      // ---- the row's sum over its four threads, the sink, the output
-      const int t = ps.token(rank);
-      float inv = 0.f, lse = -INFINITY;
+      // ---- the row's sum over its four threads and the sink, for the epilogue
       if (act) {
         const int rb = ps.ntile & 1;
         sh->red[rb][part][row] = l;
-        if (part == 0) sh->bad[row] = 0;
         if (!meet()) { ok = false; break; }
-        const float lt = (sh->red[rb][0][row] + sh->red[rb][1][row]) +
-                         (sh->red[rb][2][row] + sh->red[rb][3][row]);
-        const float sk = p.sink ? __ldg(p.sink + row) * kLog2e : -INFINITY;
-        const float M = fmaxf(m, sk), Ms = M == -INFINITY ? 0.f : M;
-        const float em = m == -INFINITY ? 0.f : fast_exp2(m - Ms);
-        const float den = lt * em + fast_exp2(sk - Ms);
-        inv = den == 0.f ? 0.f : em / den;
-        lse = den == 0.f ? -INFINITY : (Ms + fast_log2(den)) * kLn2;
-      }
-      if (!warp_wait(&sh->pvdone, (npv - 1) & 1, lim)) { ok = false; break; }
-      tc_fence_after();
-      if (act) {
-        __nv_bfloat16* const o = p.out + ((int64_t)t * kH + row) * p.dv;
-        float finite = 0.f;
-#pragma unroll 1
-        for (int c = 0; c < p.nvb * 64; c += 32) {
-          if (((c >> 5) & 1) != ch) continue;
-          // TMEM column -> Dv column: blocks of 256 split over the lane halves
-          const int b = c >> 7, wide = 2 * b + 1 < p.nvb ? 128 : 64;
-          const int d = 256 * b + hi * wide + (c - 128 * b);
-          uint32_t w[32];
-          tmem_ld32(lane_base + c, w);
-          tmem_ld_wait();
-          reg_fence(w);
-          if (d >= p.dv) continue;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t v[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float a = __uint_as_float(w[8 * q + 2 * k]) * inv;
-              const float c1 = __uint_as_float(w[8 * q + 2 * k + 1]) * inv;
-              finite = fmaf(a, 0.f, fmaf(c1, 0.f, finite));  // NaN from NaN and infinities
-              __nv_bfloat162 pr = __floats2bfloat162_rn(a, c1);
-              v[k] = *reinterpret_cast<uint32_t*>(&pr);
-            }
-            reinterpret_cast<uint4*>(o + d)[q] = make_uint4(v[0], v[1], v[2], v[3]);
-          }
+        if (part == 0) {
+          const float lt = (sh->red[rb][0][row] + sh->red[rb][1][row]) +
+                           (sh->red[rb][2][row] + sh->red[rb][3][row]);
+          const float sk = p.sink ? __ldg(p.sink + row) * kLog2e : -INFINITY;
+          const float M = fmaxf(m, sk), Ms = M == -INFINITY ? 0.f : M;
+          const float em = m == -INFINITY ? 0.f : fast_exp2(m - Ms);
+          const float den = lt * em + fast_exp2(sk - Ms);
+          sh->inv[npass & 1][row] = den == 0.f ? 0.f : em / den;
+          p.lse[(int64_t)ps.token(rank) * kH + row] =
+              den == 0.f ? -INFINITY : (Ms + fast_log2(den)) * kLn2;
         }
-        if (finite != 0.f) sh->bad[row] = 1;
-        tell_leader(&sh->oempty);
-        if (!meet()) { ok = false; break; }
-        if (part == 0)
-          p.lse[(int64_t)t * kH + row] = sh->bad[row] ? __int_as_float(0x7fffffff) : lse;
-      } else {
-        tell_leader(&sh->oempty);
       }
+      ++npass;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->stat);
     }
     if (!ok && lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 80;");
+    if (warp == kKProd || warp == kVProd) {
+      // ------------------------------------------------------------ producers
+      const bool is_v = warp == kVProd;
+      uint64_t* const fullb = is_v ? sh->vfull : sh->kfull;
+      uint64_t* const emptyb = is_v ? sh->vempty : sh->kempty;
+      uint8_t* const ring = is_v ? vring : kring;
+      const int slots = is_v ? kVSlots : kKSlots, slot_bytes = is_v ? kVSlot : kKSlot;
+      const CUtensorMap* const big = is_v ? &vmap : &kmap;
+      const CUtensorMap* const small = is_v ? &vmap16 : &kmap16;
+      int slot = 0;
+      uint32_t ph = 0, qph = 0;
+      bool first_pass = true;
+      // a free slot, armed by the leader for both CTAs' bytes
+      auto claim = [&](int bytes) -> bool {
+        if (!warp_wait(&emptyb[slot], ph ^ 1, lim)) return false;
+        if (leader && lane == 0) mbar_expect_tx(&fullb[slot], 2 * bytes);
+        __syncwarp();
+        return true;
+      };
+      auto next = [&]() {
+        if (++slot == slots) {
+          slot = 0;
+          ph ^= 1;
+        }
+      };
+      while (ok && walk.next(ps, leader && !is_v ? p.status : nullptr)) {
+        if (!is_v) {  // Q chunks, each once the pass before has read it
+          for (int c = 0; c < p.nck && ok; ++c) {
+            if (!first_pass && !warp_wait(&sh->qempty[c], qph ^ 1, lim)) { ok = false; break; }
+            if (lane == 0) {
+              if (leader) mbar_expect_tx(&sh->qfull[c], 2 * kQChunk);
+              tma_pair_3d(qbuf + c * kQChunk, &qmap, leader_addr(&sh->qfull[c]), c * 64, 0,
+                          ps.token(rank));
+            }
+            __syncwarp();
+          }
+          first_pass = false;
+          qph ^= 1;
+        }
+        for (int i = 0; i < ps.ntile && ok; ++i) {
+          const int n = ps.keys(i);
+          if (!is_v) {
+            const int s0 = 256 * i + rank * (n / 2), rows = n / 2;
+            const int per = 128 / rows;  // chunks of a slot: more where a tile has fewer keys
+            for (int c = 0; c < p.nck && ok; c += per, next()) {
+              const int cnt = min(per, p.nck - c);
+              if (!claim(cnt * rows * 128)) { ok = false; break; }
+              load_rows(ps, big, small, ring + slot * slot_bytes, leader_addr(&fullb[slot]), s0, rows,
+                        c * 64, lane, cnt, rows * 128);
+            }
+          } else {
+            for (int b = 0; b < p.nvb && ok; b += 2) {
+              // 256 columns: 128 (two panels) of each CTA; a last odd block: 64 of each
+              const int panels = b + 1 < p.nvb ? 2 : 1;
+              const int col = b * 128 + rank * panels * 64;
+              for (int k0 = 0; k0 < n && ok; k0 += 128, next()) {
+                const int rows = min(128, n - k0);
+                if (!claim(rows * 128 * panels)) { ok = false; break; }
+                load_rows(ps, big, small, ring + slot * slot_bytes, leader_addr(&fullb[slot]),
+                          256 * i + k0, rows, col, lane, panels, 16384);
+              }
+            }
+          }
+        }
+      }
+      if (!ok) {
+        // The leader's barriers count both CTAs' copies and its issuers wait for
+        // all of them; after a timeout they do not, so copies still under way get
+        // a millisecond to land before the CTA may exit.
+        if (lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
+        for (const uint64_t from = global_ns(); global_ns() - from < 1000000;) {
+        }
+      }
+    } else if (warp == kQkWarp || warp == kPvWarp) {
+      // ------------------------------------------------------------ MMA issuers
+      if (leader) {
+        const bool is_pv = warp == kPvWarp;
+        const uint64_t k_desc = umma_desc_sw128(smem_u32(kring), 16, 1024);
+        const uint64_t q_desc = umma_desc_sw128(smem_u32(qbuf), 16, 1024);
+        const uint64_t v_desc = umma_desc_sw128(smem_u32(vring), 16384, 1024);
+        const uint64_t p_desc = umma_desc_sw128(smem_u32(pbuf), 16, 1024);
+        int slot = 0;
+        uint32_t ph = 0, sidx = 0, npv = 0, npass = 0;
+        while (ok && walk.next(ps, nullptr)) {
+          for (int i = 0; i < ps.ntile && ok; ++i) {
+            const int n = ps.keys(i);
+            if (!is_pv) {
+              const uint32_t id = idesc_bf16_f32(128, n, false, false);
+              const uint32_t buf = sidx & 1, d = tmem + kSCol + buf * 128;
+              if (!warp_wait(&sh->sempty[buf], ((sidx >> 1) & 1) ^ 1, lim)) { ok = false; break; }
+              tc_fence_after();
+              const int rows = n / 2, per = 128 / rows;
+              for (int c0 = 0; c0 < p.nck; c0 += per) {
+                if (!warp_wait(&sh->kfull[slot], ph, lim)) { ok = false; break; }
+                tc_fence_after();
+                for (int c = c0; c < min(p.nck, c0 + per); ++c) {
+                  if (i == 0 && !warp_wait(&sh->qfull[c], npass & 1, lim)) { ok = false; break; }
+                  const uint64_t a = q_desc + (uint64_t)((c * kQChunk) >> 4);
+                  const uint64_t b = k_desc + (uint64_t)((slot * kKSlot + (c - c0) * rows * 128) >> 4);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    umma_pair(d, a + 2 * k, b + 2 * k, id, (c > 0 || k > 0) ? 1u : 0u);
+                  if (i + 1 == ps.ntile) commit_pair(&sh->qempty[c]);
+                }
+                commit_pair(&sh->kempty[slot]);
+                if (++slot == kKSlots) {
+                  slot = 0;
+                  ph ^= 1;
+                }
+              }
+              if (!ok) break;
+              commit_pair(&sh->sfull[buf]);
+              ++sidx;
+            } else {
+              if (!warp_wait(&sh->pfull, npv & 1, lim) ||
+                  (i == 0 && npass > 0 && !warp_wait(&sh->oempty, (npass - 1) & 1, lim))) {
+                ok = false;
+                break;
+              }
+              tc_fence_after();
+              for (int b = 0; b < p.nvb && ok; b += 2) {
+                const uint32_t id = idesc_bf16_f32(128, b + 1 < p.nvb ? 256 : 128, false, true);
+                for (int k0 = 0; k0 < n; k0 += 128) {
+                  if (!warp_wait(&sh->vfull[slot], ph, lim)) { ok = false; break; }
+                  tc_fence_after();
+                  const uint64_t v = v_desc + (uint64_t)((slot * kVSlot) >> 4);
+                  const uint64_t a = p_desc + (uint64_t)(((k0 >> 6) * kPPanel) >> 4);
+                  const int steps = min(128, n - k0) / 16;
+                  if (steps == 8) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                      umma_pair(tmem + b * 64, a + (uint64_t)(((k >> 2) * kPPanel) >> 4) + 2 * (k & 3),
+                                v + (uint64_t)(k * 128), id, (i > 0 || k0 > 0 || k > 0) ? 1u : 0u);
+                  } else {
+                    for (int k = 0; k < steps; ++k)
+                      umma_pair(tmem + b * 64, a + (uint64_t)(((k >> 2) * kPPanel) >> 4) + 2 * (k & 3),
+                                v + (uint64_t)(k * 128), id, (i > 0 || k0 > 0 || k > 0) ? 1u : 0u);
+                  }
+                  commit_pair(&sh->vempty[slot]);
+                  if (++slot == kVSlots) {
+                    slot = 0;
+                    ph ^= 1;
+                  }
+                }
+              }
+              if (!ok) break;
+              commit_pair(&sh->pvdone);
+              ++npv;
+            }
+          }
+          ++npass;
+        }
+        if (!ok && lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
+        commit_pair(&sh->drain[is_pv]);  // every MMA done before TMEM is released
+        (void)warp_wait(&sh->drain[is_pv], 0, kDefaultWaitNs);
+      }
+    } else {
+      // ------------------------------------------------------------ epilogue
+      // Thread: TMEM lane 32 g4 + lane, all its columns.  O is normalised,
+      // turned in this warp's 2 KB of shared memory and stored 64 bytes of a
+      // row at a time, while the softmax warps are in the next pass.
+      const int g4 = warp & 3, hi = g4 >> 1, row0 = 32 * (g4 & 1);
+      const uint32_t lane_base = tmem + ((uint32_t)(32 * g4) << 16);
+      uint8_t* const st = stage + g4 * kStage;
+      uint32_t npass = 0, npv = 0;
+      while (ok && walk.next(ps, nullptr)) {
+        npv += ps.ntile;
+        if (!warp_wait(&sh->stat, npass & 1, lim) || !warp_wait(&sh->pvdone, (npv - 1) & 1, lim)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (ps.active(rank)) {
+          const int64_t th = (int64_t)ps.token(rank) * kH + row0;
+          const float inv = sh->inv[npass & 1][row0 + lane];
+          float finite = 0.f;
+#pragma unroll 1
+          for (int c = 0; c < p.nvb * 64; c += 32) {
+            // TMEM column -> Dv column: blocks of 256 split over the lane halves
+            const int b = c >> 7, wide = 2 * b + 1 < p.nvb ? 128 : 64;
+            const int d = 256 * b + hi * wide + (c - 128 * b);
+            uint32_t w[32];
+            tmem_ld32(lane_base + c, w);
+            tmem_ld_wait();
+            reg_fence(w);
+            if (d >= p.dv) continue;
+            __syncwarp();
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              uint32_t v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const float a = __uint_as_float(w[8 * q + 2 * k]) * inv;
+                const float c1 = __uint_as_float(w[8 * q + 2 * k + 1]) * inv;
+                finite = fmaf(a, 0.f, fmaf(c1, 0.f, finite));  // NaN from NaN and infinities
+                __nv_bfloat162 pr = __floats2bfloat162_rn(a, c1);
+                v[k] = *reinterpret_cast<uint32_t*>(&pr);
+              }
+              // unit q of row `lane`: 8 rows' units fall into 8 different bank groups
+              *reinterpret_cast<uint4*>(st + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(v[0], v[1], v[2], v[3]);
+            }
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const int rr = 8 * j + (lane >> 2), q = lane & 3;
+              *reinterpret_cast<uint4*>(p.out + (th + rr) * p.dv + d + 8 * q) =
+                  *reinterpret_cast<const uint4*>(st + rr * 64 + ((q ^ ((rr >> 1) & 3)) << 4));
+            }
+          }
+          // a row that is not finite: launch_simt_redo computes it again
+          if (finite != 0.f) p.lse[th + lane] = __int_as_float(0x7fffffff);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) arrive_leader(&sh->oempty);
+        ++npass;
+      }
+      if (!ok && lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
+    }
   }
   // neither CTA leaves, or frees TMEM, while the other's MMAs and copies may
   // still touch it
