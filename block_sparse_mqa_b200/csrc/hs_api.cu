@@ -211,13 +211,13 @@ int hs_path(int op, hs_dtype dtype, int num_heads, int dk, int dv, int block_siz
       return !g_force_simt.load() && hs::tc_first_shape_ok(dtype, num_heads, dk, dv)
                  ? HS_PATH_TCGEN05
                  : HS_PATH_SIMT;
-    case HS_OP_SWA_FIRST_MQA_BWD: return HS_PATH_SIMT;
     case HS_OP_KV4_MQA_DECODE:
       return !g_force_simt.load() && hs::tc_kv4_decode_shape_ok(num_heads, dk, dv, dtype)
                  ? HS_PATH_TCGEN05
                  : HS_PATH_SIMT;
     case HS_OP_SPARSE_MQA_BWD:
     case HS_OP_SWA_MQA_BWD:
+    case HS_OP_SWA_FIRST_MQA_BWD:
       if (!g_force_simt.load() && hs::tc_backward_shape_ok(dtype, num_heads, dk, dv))
         return HS_PATH_MMA;
       return HS_PATH_SIMT;
@@ -693,6 +693,7 @@ hs_status hs_swa_first_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_he
   a.block_size = 64;
   a.window = window;
   a.first = num_first;
+  a.with_first = true;
   a.grad_like_input = true;
   return backward_common(a, false, q, q_row_stride, q_head_stride, k, k_row_stride, v,
                          v_row_stride, cu_seqlens, num_docs, total_tokens, max_seqlen, num_heads,

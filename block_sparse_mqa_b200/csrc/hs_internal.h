@@ -79,6 +79,7 @@ struct BwdArgs {
   void* dval;
   float* dsink;        // may be null
   int first = 0;       // swa only: first tokens of the document that stay visible
+  bool with_first = false;       // the call is hs_swa_first_mqa_bwd (first may be 0)
   bool grad_like_input = false;  // dq, dkey, dval in p.dtype instead of fp32
   void* workspace;     // simt_backward_workspace() bytes
   void* dkdv_ws;       // the tensor-core dk / dv pass's partial sums, or null
@@ -112,7 +113,8 @@ bool tc_bwd_dq_supported(const Problem& p);
 bool tc_bwd_dkdv_supported(const Problem& p);
 // Bytes of the dk / dv pass's partial sums (per query range, per key row).
 size_t tc_bwd_dkdv_workspace(int total_tokens, int dk, int dv);
-cudaError_t launch_tc_bwd_dq(const BwdArgs& a, bool sparse, const float* delta,
+// `spoiled` (may be null): set to 1 per token whose dq is not finite.
+cudaError_t launch_tc_bwd_dq(const BwdArgs& a, bool sparse, const float* delta, int* spoiled,
                              long long wait_limit, cudaStream_t s);
 cudaError_t launch_tc_bwd_dkdv(const BwdArgs& a, bool sparse, const float* delta,
                                long long wait_limit, cudaStream_t s);

@@ -52,6 +52,7 @@ struct BwdParams {
   float* delta;       // workspace [T, H]
   float* dsink_part;  // workspace [T, H]
   int G, KT;          // heads per group, keys per dq tile
+  const int* only;    // dq of the tokens with only[t] != 0 alone (null: all)
 };
 
 template <typename T>
@@ -148,6 +149,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
   int* blist = reinterpret_cast<int*>(del_s + G);
   const float scale = P.scale;
   for (int t = blockIdx.x; t < P.total_tokens; t += gridDim.x) {
+    if (a.only && __ldg(a.only + t) == 0) continue;
     int bos, eos;
     if (!find_doc(P.cu_seqlens, P.num_docs, P.total_tokens, P.max_seqlen, t, bos, eos,
                   P.status))
@@ -406,6 +408,27 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
 
 constexpr size_t kMaxSmem = 227 * 1024;
 
+// dq: the largest head group (and key tile) whose staging fits.
+template <typename T, bool kSparse>
+cudaError_t launch_dq(BwdParams a, cudaStream_t s) {
+  const Problem& P = a.p;
+  int G = 16, KT = 16;
+  const size_t ints = 256 * sizeof(int);
+  while (G > 1 && dq_smem_floats(G, KT, P.dk, P.dv) * 4 + ints > kMaxSmem) G >>= 1;
+  while (KT > 1 && dq_smem_floats(G, KT, P.dk, P.dv) * 4 + ints > kMaxSmem) KT >>= 1;
+  const size_t bytes = dq_smem_floats(G, KT, P.dk, P.dv) * 4 + ints;
+  if (bytes > kMaxSmem) return cudaErrorInvalidConfiguration;
+  a.G = G;
+  a.KT = KT;
+  auto kern = bwd_dq_kernel<T, kSparse>;
+  cudaError_t e =
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e != cudaSuccess) return e;
+  const int grid = a.only && P.total_tokens > 592 ? 592 : P.total_tokens;
+  kern<<<grid, kThreads, bytes, s>>>(a);
+  return cudaGetLastError();
+}
+
 template <typename T, bool kSparse>
 cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
   const Problem& P = a.p;
@@ -419,22 +442,9 @@ cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
-  // dq: the largest head group (and key tile) whose staging fits (unless the
-  // caller runs the tensor-core passes instead)
+  // (the caller runs the tensor-core passes instead of these)
   if (cuda_core_passes) {
-    int G = 16, KT = 16;
-    const size_t ints = 256 * sizeof(int);
-    while (G > 1 && dq_smem_floats(G, KT, P.dk, P.dv) * 4 + ints > kMaxSmem) G >>= 1;
-    while (KT > 1 && dq_smem_floats(G, KT, P.dk, P.dv) * 4 + ints > kMaxSmem) KT >>= 1;
-    const size_t bytes = dq_smem_floats(G, KT, P.dk, P.dv) * 4 + ints;
-    if (bytes > kMaxSmem) return cudaErrorInvalidConfiguration;
-    a.G = G;
-    a.KT = KT;
-    auto kern = bwd_dq_kernel<T, kSparse>;
-    e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e != cudaSuccess) return e;
-    kern<<<NT, kThreads, bytes, s>>>(a);
-    e = cudaGetLastError();
+    e = launch_dq<T, kSparse>(a, s);
     if (e != cudaSuccess) return e;
   }
   // dk, dv: key tiles of at most kKeyTile keys (unless the caller runs the
@@ -484,14 +494,27 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
   a.dsink_part = a.delta + (size_t)b.p.total_tokens * b.p.num_heads;
   if (b.p.dtype == HS_BF16) {
     // tensor cores: dq and dk / dv on tcgen05 (else every pass on CUDA cores)
-    const bool mma = allow_mma && b.first == 0 && !b.grad_like_input && tc_bwd_dq_supported(b.p) && tc_bwd_dkdv_supported(b.p) &&
+    const bool mma = allow_mma && tc_bwd_dq_supported(b.p) && tc_bwd_dkdv_supported(b.p) &&
                      (reinterpret_cast<uintptr_t>(b.dout) & 15) == 0 && b.dkdv_ws != nullptr;
     if (path) *path = mma ? HS_PATH_MMA : HS_PATH_SIMT;
     cudaError_t e = sparse ? launch_typed<__nv_bfloat16, true>(a, !mma, s)
                            : launch_typed<__nv_bfloat16, false>(a, !mma, s);
     if (e != cudaSuccess || !mma) return e;
-    e = launch_tc_bwd_dq(b, sparse, a.delta, 0, s);
+    // With visible first tokens nothing outside the key sets may show: a dq
+    // that a key outside spoiled (0 * NaN in a whole-tile product) is flagged
+    // and computed again.  The sink terms' place is free for the flags.
+    int* const flags = b.with_first ? reinterpret_cast<int*>(a.dsink_part) : nullptr;
+    if (flags) {
+      e = cudaMemsetAsync(flags, 0, sizeof(int) * (size_t)b.p.total_tokens, s);
+      if (e != cudaSuccess) return e;
+    }
+    e = launch_tc_bwd_dq(b, sparse, a.delta, flags, 0, s);
     if (e != cudaSuccess) return e;
+    if (flags) {
+      a.only = flags;
+      e = launch_dq<__nv_bfloat16, false>(a, s);
+      if (e != cudaSuccess) return e;
+    }
     return launch_tc_bwd_dkdv(b, sparse, a.delta, 0, s);
   }
   if (path) *path = HS_PATH_SIMT;

@@ -65,12 +65,14 @@ struct DkdvParams {
   int num_docs, T, max_seqlen;
   const int32_t* idx;
   int topk, B, window;
+  int first;           // window: first tokens of each document that stay visible
   int nck, ndc, dk, dv;
   float scale, scale_log2;
   const float* lse;
   const float* delta;
-  float* dkey;
-  float* dval;
+  void* dkey;          // fp32, or bf16 (like_input)
+  void* dval;
+  bool like_input;
   int* status;
   long long wait_ns;
   // work items: (32-key tile, query range) pairs, range-major
@@ -80,12 +82,13 @@ struct DkdvParams {
 };
 
 // The tiles whose keys a query in [r0, r1) can attend: every earlier tile for
-// block-sparse attention, the tiles within one window before it for SWA.
-__host__ __device__ __forceinline__ void range_tiles(bool sparse, int rg, int rlen, int T,
+// block-sparse attention and where first tokens stay visible (`all`), the tiles
+// within one window before it for SWA.
+__host__ __device__ __forceinline__ void range_tiles(bool all, int rg, int rlen, int T,
                                                      int window, int& tlo, int& thi) {
   const int r0 = rg * rlen, r1 = min(T, r0 + rlen);
   thi = (r1 + kKT - 1) / kKT;
-  tlo = sparse ? 0 : max(0, (r0 - window - kKT + 1) / kKT);
+  tlo = all ? 0 : max(0, (r0 - window - kKT + 1) / kKT);
   if (tlo > thi) tlo = thi;
 }
 
@@ -93,11 +96,11 @@ __host__ __device__ __forceinline__ void range_tiles(bool sparse, int rg, int rl
 // same time take members from the same range of queries (whose q_t and
 // dout_t then stay in L2), and a tile every query selects is spread over all
 // ranges instead of one cluster.
-__host__ __device__ __forceinline__ bool item_of(bool sparse, int k, int rlen, int nrange, int T,
+__host__ __device__ __forceinline__ bool item_of(bool all, int k, int rlen, int nrange, int T,
                                                  int window, int& tile, int& rg) {
   for (rg = 0; rg < nrange; ++rg) {
     int tlo, thi;
-    range_tiles(sparse, rg, rlen, T, window, tlo, thi);
+    range_tiles(all, rg, rlen, T, window, tlo, thi);
     if (k < thi - tlo) {
       tile = tlo + k;
       return true;
@@ -222,7 +225,7 @@ tc_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap kmap,
   // barrier.  A CTA that gave up skips its members' work.
   for (int item = blockIdx.x / csize; item < p.nitems; item += ncl) {
     int tile, rg;
-    if (!item_of(kSparse, item, p.rlen, p.nrange, NT, p.window, tile, rg)) break;
+    if (!item_of(kSparse || p.first > 0, item, p.rlen, p.nrange, NT, p.window, tile, rg)) break;
     const int r0 = rg * p.rlen, r1 = min(NT, r0 + p.rlen);  // this item's queries
     const int j1 = min(NT, tile * kKT + kKT);
     for (int s0 = tile * kKT; s0 < j1;) {  // one document segment at a time
@@ -231,7 +234,7 @@ tc_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap kmap,
       if (!find_doc(p.cu, p.num_docs, NT, p.max_seqlen, s0, bos, eos, p.status)) break;
       const int s1 = min(j1, eos), n = s1 - s0;
       // the segment's candidate queries [s0, tend) inside this item's range
-      const int tend_all = kSparse ? eos : min(eos, s1 - 1 + p.window);
+      const int tend_all = kSparse || s0 - bos < p.first ? eos : min(eos, s1 - 1 + p.window);
       const int c_lo = max(s0, r0), tend = min(tend_all, r1);
       if (c_lo >= tend) {  // none: no partial sum for this segment and range
         s0 = s1;
@@ -270,7 +273,7 @@ tc_bwd_dkdv_kernel(const __grid_constant__ CUtensorMap kmap,
           } else {
             for (int jj = 0; jj < n; ++jj) {
               const int j = s0 + jj;
-              if (j <= t && j > t - p.window) mask |= 1u << jj;
+              if (j <= t && (j > t - p.window || j - bos < p.first)) mask |= 1u << jj;
             }
           }
         }
@@ -558,14 +561,17 @@ __global__ void __launch_bounds__(256) dkdv_reduce_kernel(const DkdvParams p) {
     if (find_doc(p.cu, p.num_docs, p.T, p.max_seqlen, j, bos, eos, nullptr)) {
       const int tile0 = (j / kKT) * kKT;
       const int s0 = max(bos, tile0), s1 = min(tile0 + kKT, eos);
-      const int tend = kSparse ? eos : min(eos, s1 - 1 + p.window);
+      const int tend = kSparse || s0 - bos < p.first ? eos : min(eos, s1 - 1 + p.window);
       for (int rg = s0 / p.rlen; rg < p.nrange && rg * p.rlen < tend; ++rg)
         sum += __ldcs(p.part + ((int64_t)rg * p.T + j) * W + col);
     }
-    if (col < p.dk)
-      p.dkey[(int64_t)j * p.dk + col] = p.scale * sum;
+    void* const dst = col < p.dk ? p.dkey : p.dval;
+    const int64_t at = col < p.dk ? (int64_t)j * p.dk + col : (int64_t)j * p.dv + (col - p.dk);
+    if (col < p.dk) sum *= p.scale;
+    if (p.like_input)
+      static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(sum);
     else
-      p.dval[(int64_t)j * p.dv + (col - p.dk)] = sum;
+      static_cast<float*>(dst)[at] = sum;
   }
 }
 
@@ -637,6 +643,7 @@ cudaError_t launch_tc_bwd_dkdv(const BwdArgs& b, bool sparse, const float* delta
   a.topk = b.topk;
   a.B = b.block_size;
   a.window = b.window;
+  a.first = b.first;
   a.nck = p.dk / 64;
   a.ndc = p.dv / 64;
   a.dk = p.dk;
@@ -645,15 +652,16 @@ cudaError_t launch_tc_bwd_dkdv(const BwdArgs& b, bool sparse, const float* delta
   a.scale_log2 = p.scale * kLog2e;
   a.lse = b.lse;
   a.delta = delta;
-  a.dkey = static_cast<float*>(b.dkey);
-  a.dval = static_cast<float*>(b.dval);
+  a.dkey = b.dkey;
+  a.dval = b.dval;
+  a.like_input = b.grad_like_input;
   a.status = p.status;
   a.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
   range_split(p.total_tokens, a.rlen, a.nrange);
   a.nitems = 0;
   for (int rg = 0; rg < a.nrange; ++rg) {
     int tlo, thi;
-    range_tiles(sparse, rg, a.rlen, p.total_tokens, a.window, tlo, thi);
+    range_tiles(sparse || a.first > 0, rg, a.rlen, p.total_tokens, a.window, tlo, thi);
     a.nitems += thi - tlo;
   }
   a.part = static_cast<float*>(b.dkdv_ws);

@@ -59,11 +59,14 @@ struct DqParams {
   int num_docs, T, max_seqlen;
   const int32_t* idx;
   int topk, B, window;
+  int first;  // window: first tokens of the document that stay visible
   int nck, ndc, dk;
   float scale, scale_log2;
   const float* lse;
   const float* delta;
-  float* dq;
+  int* spoiled;  // may be null
+  void* dq;      // fp32, or bf16 (like_input)
+  bool like_input;
   int* status;
   long long wait_ns;
 };
@@ -98,6 +101,7 @@ __device__ __forceinline__ void give_up(Shared* sh, int* status) {
 struct TokenPlan {
   bool ok;
   int bos, bq, wlo, nsel, ntile;
+  int nf, nft;  // window: first tokens before it, and their tiles (which come first)
 };
 
 // The forward's index rule: entry s is used when 0 <= b <= bq and b is larger
@@ -116,6 +120,7 @@ __device__ __forceinline__ TokenPlan plan_token(const DqParams& p, int t) {
   tp.wlo = 0;
   tp.nsel = 0;
   tp.ntile = 0;
+  tp.nf = tp.nft = 0;
   if (!tp.ok) return tp;
   if (kSparse) {
     const int32_t* row = p.idx + (int64_t)t * p.topk;
@@ -129,7 +134,9 @@ __device__ __forceinline__ TokenPlan plan_token(const DqParams& p, int t) {
     tp.ntile = (n + per - 1) / per;
   } else {
     tp.wlo = max(tp.bos, t - p.window + 1);
-    tp.ntile = (t - tp.wlo + 1 + kTile - 1) / kTile;
+    tp.nf = min(p.first, tp.wlo - tp.bos);
+    tp.nft = (tp.nf + kTile - 1) / kTile;
+    tp.ntile = tp.nft + (t - tp.wlo + 1 + kTile - 1) / kTile;
   }
   return tp;
 }
@@ -261,7 +268,7 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           const int b = slotn < tp.nsel ? sh->plist[slotn] : tp.bq;
           row0 = tp.bos + b * p.B;
         } else {
-          row0 = tp.wlo + tile * kTile;
+          row0 = tile < tp.nft ? tp.bos + tile * kTile : tp.wlo + (tile - tp.nft) * kTile;
         }
         tma_load_2d(dst + pn * kPanel + j * box_rows * 128, is_v ? &vmap : &kmap, &sh->full[slot],
                     col, row0);
@@ -450,9 +457,15 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
     for (int t = blockIdx.x; t < p.T && ok && !aborted(sh); t += G) {
       const TokenPlan tp = plan_token<kSparse>(p, t);
       if (!tp.ok) continue;
-      float* const dqt = p.dq + ((int64_t)t * kH + hb) * p.dk;
+      const int64_t dqt = ((int64_t)t * kH + hb) * p.dk;
+      auto put = [&](int64_t at, float v) {
+        if (p.like_input)
+          static_cast<__nv_bfloat16*>(p.dq)[dqt + at] = __float2bfloat16_rn(v);
+        else
+          static_cast<float*>(p.dq)[dqt + at] = v;
+      };
       if (tp.ntile == 0) {  // no valid block: dq is zero
-        for (int e = r; e < 32 * p.dk; e += 128) dqt[e] = 0.f;
+        for (int e = r; e < 32 * p.dk; e += 128) put(e, 0.f);
         continue;
       }
       if (r < 32) {
@@ -497,7 +510,7 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
           const int key = tp.bos + b * p.B + (r % p.B);
           valid = slotn < tp.nsel && key <= t;
         } else {
-          valid = tp.wlo + i * kTile + r <= t;
+          valid = i < tp.nft ? i * kTile + r < tp.nf : tp.wlo + (i - tp.nft) * kTile + r <= t;
         }
         uint32_t pk[16];
 #pragma unroll
@@ -530,6 +543,7 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
       // ---------------- epilogue: dq[t, h, :] = scale * dQ^T[:, h] (fp32)
       if (!mbar_wait(&sh->dqfull, ntok & 1, lim)) { ok = false; break; }
       tc_fence_after();
+      float finite = 0.f;  // NaN from NaN and infinities
       for (int m = 0; m < nsk; ++m) {
         uint32_t w[32];
         tmem_ld32(lane_base + m * kH + hb, w);
@@ -537,10 +551,15 @@ tc_bwd_dq_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant
         reg_fence(w);
         const int d = m * 128 + r;
         if (d < p.dk) {
+          if (p.spoiled) {
 #pragma unroll
-          for (int k = 0; k < 32; ++k) dqt[(int64_t)k * p.dk + d] = p.scale * __uint_as_float(w[k]);
+            for (int k = 0; k < 32; ++k) finite = fmaf(__uint_as_float(w[k]), 0.f, finite);
+          }
+#pragma unroll
+          for (int k = 0; k < 32; ++k) put((int64_t)k * p.dk + d, p.scale * __uint_as_float(w[k]));
         }
       }
+      if (finite != 0.f) p.spoiled[t] = 1;
       tc_fence_before();
       mbar_arrive(&sh->dqempty);
       ++ntok;
@@ -566,7 +585,7 @@ bool tc_bwd_dq_supported(const Problem& p) {
          p.q_head_stride % 8 == 0 && p.k_row_stride % 8 == 0 && p.v_row_stride % 8 == 0;
 }
 
-cudaError_t launch_tc_bwd_dq(const BwdArgs& b, bool sparse, const float* delta,
+cudaError_t launch_tc_bwd_dq(const BwdArgs& b, bool sparse, const float* delta, int* spoiled,
                              long long wait_limit, cudaStream_t s) {
   const Problem& p = b.p;
   const uint32_t rows = sparse ? (uint32_t)b.block_size : (uint32_t)kTile;
@@ -608,6 +627,7 @@ cudaError_t launch_tc_bwd_dq(const BwdArgs& b, bool sparse, const float* delta,
   a.topk = b.topk;
   a.B = b.block_size;
   a.window = b.window;
+  a.first = b.first;
   a.nck = p.dk / 64;
   a.ndc = p.dv / 64;
   a.dk = p.dk;
@@ -615,7 +635,9 @@ cudaError_t launch_tc_bwd_dq(const BwdArgs& b, bool sparse, const float* delta,
   a.scale_log2 = p.scale * kLog2e;
   a.lse = b.lse;
   a.delta = delta;
-  a.dq = static_cast<float*>(b.dq);
+  a.spoiled = spoiled;
+  a.dq = b.dq;
+  a.like_input = b.grad_like_input;
   a.status = p.status;
   a.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
   auto kern = sparse ? tc_bwd_dq_kernel<true> : tc_bwd_dq_kernel<false>;
