@@ -121,10 +121,16 @@ hs_status check_problem(hs::Problem& p, const void* q, int64_t qrs, int64_t qhs,
 size_t bwd_simt_bytes(int total_tokens, int num_heads) {
   return (hs::simt_backward_workspace(total_tokens, num_heads) + 255) & ~(size_t)255;
 }
-size_t bwd_workspace(int total_tokens, int num_heads, int dk, int dv, hs_dtype dtype) {
+// span > 0: the window attention with first tokens, window + first keys.
+size_t bwd_workspace(int total_tokens, int num_heads, int dk, int dv, hs_dtype dtype,
+                     int num_docs = 0, int max_seqlen = 0, int span = 0) {
   size_t need = bwd_simt_bytes(total_tokens, num_heads);
-  if (!g_force_simt.load() && hs::tc_backward_shape_ok(dtype, num_heads, dk, dv))
-    need += hs::tc_bwd_dkdv_workspace(total_tokens, dk, dv);
+  if (!g_force_simt.load() && hs::tc_backward_shape_ok(dtype, num_heads, dk, dv)) {
+    size_t tc = hs::tc_bwd_dkdv_workspace(total_tokens, dk, dv);
+    if (span > 0)
+      tc = std::max(tc, hs::tc_first_bwd_workspace(total_tokens, num_docs, max_seqlen, span, dk, dv));
+    need += tc;
+  }
   return need;
 }
 
@@ -244,7 +250,10 @@ size_t hs_workspace_size(int op, int total_tokens, int num_docs, int max_seqlen,
   }
   if ((op == HS_OP_SPARSE_MQA_BWD || op == HS_OP_SWA_MQA_BWD || op == HS_OP_SWA_FIRST_MQA_BWD) &&
       total_tokens > 0 && num_heads > 0)
-    return bwd_workspace(total_tokens, num_heads, dk, dv, dtype);
+    return op == HS_OP_SWA_FIRST_MQA_BWD
+               ? bwd_workspace(total_tokens, num_heads, dk, dv, dtype, std::max(num_docs, 1),
+                               std::max(max_seqlen, 1), std::max(block_size, 1))
+               : bwd_workspace(total_tokens, num_heads, dk, dv, dtype);
   if ((op != HS_OP_BLOCK_SCORE && op != HS_OP_BLOCK_SCORE_ATTN) || total_tokens <= 0 ||
       !valid_block(block_size))
     return 0;
@@ -585,7 +594,9 @@ static hs_status backward_common(hs::BwdArgs& a, bool sparse, const void* q, int
   a.dval = dval;
   a.dsink = dsink;
   if (total_tokens == 0) return HS_OK;
-  const size_t need = bwd_workspace(total_tokens, num_heads, dk, dv, dtype);
+  int span = 0;  // of keys, none of them past a document
+  if (a.with_first) span = std::min(a.window, max_seqlen) + std::min(a.first, max_seqlen);
+  const size_t need = bwd_workspace(total_tokens, num_heads, dk, dv, dtype, num_docs, max_seqlen, span);
   if (!workspace || workspace_bytes < need)
     return fail(HS_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? workspace_bytes : (size_t)0);
@@ -595,6 +606,7 @@ static hs_status backward_common(hs::BwdArgs& a, bool sparse, const void* q, int
   a.dkdv_ws = need > bwd_simt_bytes(total_tokens, num_heads)
                   ? static_cast<char*>(workspace) + bwd_simt_bytes(total_tokens, num_heads)
                   : nullptr;
+  a.dkdv_bytes = need - bwd_simt_bytes(total_tokens, num_heads);
   r = status_ptr(&a.p.status);
   if (r != HS_OK) return r;
   int path = HS_PATH_SIMT;

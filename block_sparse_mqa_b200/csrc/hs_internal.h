@@ -82,7 +82,8 @@ struct BwdArgs {
   bool with_first = false;       // the call is hs_swa_first_mqa_bwd (first may be 0)
   bool grad_like_input = false;  // dq, dkey, dval in p.dtype instead of fp32
   void* workspace;     // simt_backward_workspace() bytes
-  void* dkdv_ws;       // the tensor-core dk / dv pass's partial sums, or null
+  void* dkdv_ws;       // the tensor-core passes' workspace, or null
+  size_t dkdv_bytes;
 };
 
 // Launchers; each returns cudaSuccess or the launch error.
@@ -99,6 +100,13 @@ cudaError_t launch_simt_redo(const AttnArgs& a, cudaStream_t s);
 // The window attention with visible first tokens on pairs of CTAs.
 bool tc_first_shape_ok(hs_dtype dtype, int num_heads, int dk, int dv);
 bool tc_first_eligible(const Problem& p);
+// Bytes of the backward's passes for window + first = span keys (0: they do
+// not take it); *taken = false where the workspace or the first tokens rule
+// them out.
+size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, int span, int dk,
+                              int dv);
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled, void* ws,
+                                size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s);
 cudaError_t launch_tc_first_fwd(const AttnArgs& a, long long wait_limit, cudaStream_t s);
 size_t simt_backward_workspace(int total_tokens, int num_heads);
 // *path (may be null) receives the kernel family the dq and dk / dv passes use.

@@ -508,13 +508,21 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
       e = cudaMemsetAsync(flags, 0, sizeof(int) * (size_t)b.p.total_tokens, s);
       if (e != cudaSuccess) return e;
     }
-    e = launch_tc_bwd_dq(b, sparse, a.delta, flags, 0, s);
-    if (e != cudaSuccess) return e;
+    bool taken = false;  // the window's own passes, where their workspace was given
+    if (flags) {
+      e = launch_tc_first_bwd(b, a.delta, flags, b.dkdv_ws, b.dkdv_bytes, 0, &taken, s);
+      if (e != cudaSuccess) return e;
+    }
+    if (!taken) {
+      e = launch_tc_bwd_dq(b, sparse, a.delta, flags, 0, s);
+      if (e != cudaSuccess) return e;
+    }
     if (flags) {
       a.only = flags;
       e = launch_dq<__nv_bfloat16, false>(a, s);
       if (e != cudaSuccess) return e;
     }
+    if (taken) return cudaSuccess;
     return launch_tc_bwd_dkdv(b, sparse, a.delta, 0, s);
   }
   if (path) *path = HS_PATH_SIMT;

@@ -577,8 +577,9 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
             grads[3].zero_()
         return grads
     if workspace is None:
+        span = min(int(window), int(max_seqlen)) + min(int(num_first), int(max_seqlen))
         workspace = torch.empty(workspace_size(HS_OP_SWA_FIRST_MQA_BWD, T, nd, max_seqlen, H, Dk,
-                                               Dv, q.dtype, 64),
+                                               Dv, q.dtype, span),
                                 device=q.device, dtype=torch.uint8)
     with torch.cuda.device(q.device):
         _check(lib().hs_swa_first_mqa_bwd(
