@@ -84,32 +84,45 @@ __device__ __forceinline__ float scale_value(uint32_t byte) {
   return __half2float(__ushort_as_half((unsigned short)(byte << 7)));
 }
 
-// Scale byte of a group with largest magnitude amax (finite): the smallest
-// scale s with 7 s >= amax.  The quotient is rounded up and so is its
-// significand's cut to 4 bits, so no s is one step too small.
+// Scale of a group with largest magnitude amax (finite): the smallest scale s
+// with 7 s >= amax.  A truncated product with 1/7 is at most two steps low, and
+// 7 s is exact (3 bits times 4), so the comparison decides.
 __device__ __forceinline__ float group_scale(float amax) {
-  const float r = __fdiv_ru(amax, 7.f);
+  const float r = amax * 0.142857134f;  // just under 1 / 7
   float s;
-  if (r >= 6.103515625e-05f)  // 2^-14: normal
-    s = __uint_as_float((__float_as_uint(r) + 0xfffffu) & ~0xfffffu);
-  else  // steps of 2^-17
-    s = ceilf(r * 131072.f) * 7.62939453125e-06f;
+  if (r >= 6.103515625e-05f) {  // 2^-14: normal, 4 significant bits
+    uint32_t u = __float_as_uint(r) & ~0xfffffu;
+    u += 7.f * __uint_as_float(u) < amax ? 0x100000u : 0u;
+    u += 7.f * __uint_as_float(u) < amax ? 0x100000u : 0u;
+    s = __uint_as_float(u);
+  } else {  // steps of 2^-17
+    const float step = 7.62939453125e-06f;
+    s = floorf(r * 131072.f) * step;
+    s += 7.f * s < amax ? step : 0.f;
+    s += 7.f * s < amax ? step : 0.f;
+  }
   return fminf(s, kMaxScale);
 }
 __device__ __forceinline__ uint32_t scale_byte(float s) {
   return (uint32_t)__half_as_ushort(__float2half_rn(s)) >> 7;  // exact: 4 significant bits
 }
 
-// Code of x for scale s > 0: rint(x / s), half to even, clamped to +-7, plus
-// 8.  (h + 0.5) s is exact (4 bits times 4), so the comparison decides the
-// rounding without the quotient's own rounding error.
-__device__ __forceinline__ uint32_t code_of(float x, float s) {
-  const float ax = fabsf(x);
-  if (ax >= 7.f * s) return x < 0.f ? 1u : 15u;
-  const int h = (int)__fdiv_rn(ax, s);  // 0..7
-  const float mid = ((float)h + 0.5f) * s;
-  const int n = h + ((ax > mid || (ax == mid && (h & 1))) ? 1 : 0);
-  return (uint32_t)(8 + (x < 0.f ? -n : n));
+// Low four bits: rint(x / s), half to even, as a two's complement number; |x| <=
+// 7 s, inv = 1 / s rounded.  The product's rounding can miss a border between
+// two codes, so the remainder, which is exact (a few bits beyond s), decides.
+__device__ __forceinline__ uint32_t code_bits(float x, float s, float inv) {
+  constexpr float kRound = 12582912.f;  // 1.5 * 2^23: adding it rounds to an integer
+  float y = fmaf(x, inv, kRound);
+  const float d = fmaf(kRound - y, s, x), half = 0.5f * s;
+  if (fabsf(d) > half || (fabsf(d) == half && (__float_as_uint(y) & 1u))) y += copysignf(1.f, d);
+  return __float_as_uint(y) & 15u;
+}
+// Eight codes (rint + 8) in the order of a word.
+__device__ __forceinline__ uint32_t code_word(const float (&x)[8], float s, float inv) {
+  uint32_t w = 0u;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w |= code_bits(x[e], s, inv) << (4 * (e >> 1) + 16 * (e & 1));
+  return w ^ 0x88888888u;  // n mod 16 -> n + 8
 }
 
 }  // namespace kv4

@@ -6,10 +6,12 @@
 // A group with a NaN or an infinity gets the NaN scale, so that it reads as
 // NaN and is not hidden; a scale past the format's range saturates.
 //
-// Both are bound by memory: one thread owns one group of one row, reads its 64
-// bytes (bf16) or 16 bytes of codes once and writes the other form once.
-// Neighbouring threads take neighbouring groups of a row, whose elements are
-// contiguous.
+// Both are bound by memory (and by latency for a few rows): an element is read
+// once and its code written once.  A block takes 8 consecutive rows, looks up
+// where they live once, and its 8 warps take the groups: four lanes share a
+// group (8 elements, 16 bytes of bf16, one word of codes each), eight rows
+// side by side, so that a warp reads eight runs of 64 bytes and writes one of
+// 128 (the codes of a group of consecutive rows are contiguous).
 
 #include "kv4.cuh"
 
@@ -17,36 +19,57 @@ namespace hs {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kBatch = 3;  // groups of a thread whose loads go together
 
-// Where row i of the packed rows lives: sequence s with cu[s] <= i < cu[s+1],
-// cached position seq_lens[s] - (cu[s+1] - i).  False: a padding row behind
-// the last sequence (silent) or a malformed input (recorded).
-__device__ __forceinline__ bool locate(const Kv4Rows& a, int64_t i, int& page, int& slot) {
-  if (i >= __ldg(a.cu + a.num_seqs)) return false;  // behind the last sequence
-  int lo = 0, hi = a.num_seqs;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(a.cu + mid) <= i) lo = mid; else hi = mid;
+// A block's rows: where each lives (page -1: nowhere).
+template <int kRows>
+struct Rows {
+  int page[kRows], slot[kRows];
+};
+
+// Row i of the packed rows belongs to sequence s with cu[s] <= i < cu[s+1] and
+// is its cached position seq_lens[s] - (cu[s+1] - i).  The block counts the
+// sequences that end at or before its first row (one round of loads for up to
+// 256 of them, where a search would wait for each of its steps), and each row
+// steps on from there.  Rows behind the last sequence are padding (silent); a
+// malformed input is recorded.
+template <int kRows>
+__device__ __forceinline__ void locate_rows(const Kv4Rows& a, int64_t row0, Rows<kRows>& sh) {
+  int before = 0;
+  for (int s0 = 0; s0 < a.num_seqs; s0 += kThreads) {
+    const int s = s0 + threadIdx.x;
+    before += __syncthreads_count(s < a.num_seqs && __ldg(a.cu + s + 1) <= row0);
   }
-  const int bos = __ldg(a.cu + lo), eos = __ldg(a.cu + lo + 1);
-  const int len = __ldg(a.seq_lens + lo);
-  if (bos < 0 || i < bos || i >= eos || eos > a.total_tokens || len < eos - bos) {
-    record_status(a.status, HS_ERR_INVALID_ARG);
-    return false;
+  if (threadIdx.x < kRows) {
+    const int64_t i = row0 + threadIdx.x;
+    int page = -1, slot = 0;
+    if (i < a.total_tokens && i < __ldg(a.cu + a.num_seqs)) {
+      int s = before;
+      while (s < a.num_seqs && __ldg(a.cu + s + 1) <= i) ++s;
+      const int bos = s < a.num_seqs ? __ldg(a.cu + s) : -1;
+      const int eos = s < a.num_seqs ? __ldg(a.cu + s + 1) : -1;
+      const int len = s < a.num_seqs ? __ldg(a.seq_lens + s) : 0;
+      if (bos < 0 || i < bos || eos > a.total_tokens || len < eos - bos) {
+        record_status(a.status, HS_ERR_INVALID_ARG);
+      } else {
+        const int pos = len - (int)(eos - i);
+        slot = pos & ((1 << a.ps_log2) - 1);
+        page = kv4::page_of(a.table + (int64_t)s * a.table_stride, a.table_width, a.num_pages, pos,
+                            a.ps_log2, a.status);
+      }
+    }
+    sh.page[threadIdx.x] = page;
+    sh.slot[threadIdx.x] = slot;
   }
-  const int pos = len - (int)(eos - i);
-  slot = pos & ((1 << a.ps_log2) - 1);
-  page = kv4::page_of(a.table + (int64_t)lo * a.table_stride, a.table_width, a.num_pages, pos,
-                      a.ps_log2, a.status);
-  return page >= 0;
+  __syncthreads();
 }
 
 template <typename T, bool kVec>
-__device__ __forceinline__ void load_group(const T* p, float (&x)[32]) {
+__device__ __forceinline__ void load8(const T* p, float (&x)[8]) {
   if (kVec) {
     constexpr int kPer = 16 / sizeof(T);
 #pragma unroll
-    for (int u = 0; u < 32 / kPer; ++u) {
+    for (int u = 0; u < 8 / kPer; ++u) {
       const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + u);
       const T* e = reinterpret_cast<const T*>(&w);
 #pragma unroll
@@ -54,121 +77,148 @@ __device__ __forceinline__ void load_group(const T* p, float (&x)[32]) {
     }
   } else {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) x[j] = to_f32<T>(p[j]);
+    for (int j = 0; j < 8; ++j) x[j] = to_f32<T>(p[j]);
   }
 }
 
-// Groups of the k rows and, behind them, of the v rows: item = row * (Gk + Gv) + group.
-template <typename T, bool kVec>
+// Groups of the k rows and, behind them, of the v rows.
+template <typename T, bool kVec, int kRows>
 __global__ void __launch_bounds__(kThreads) kv4_append_kernel(const Kv4Rows a, const Kv4Append w) {
-  const int gk = kv4::groups(w.dk), gv = kv4::groups(w.dv), G = gk + gv;
-  const int ps = 1 << a.ps_log2;
-  const int64_t total = (int64_t)a.total_tokens * G;
-  for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < total;
-       it += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = it / G;
-    const int gg = (int)(it - i * G);
-    int page, slot;
-    if (!locate(a, i, page, slot)) continue;
-    const bool is_v = gg >= gk;
-    const int g = is_v ? gg - gk : gg;
-    const T* src = is_v ? static_cast<const T*>(w.v) + i * w.v_row_stride
-                        : static_cast<const T*>(w.k) + i * w.k_row_stride;
-    float x[32];
-    load_group<T, kVec>(src + g * 32, x);
-    float amax = 0.f;
-    bool finite = true;
+  __shared__ Rows<kRows> sh;
+  const int64_t row0 = (int64_t)blockIdx.x * kRows;
+  locate_rows(a, row0, sh);
+  const int gk = kv4::groups(w.dk), G = gk + kv4::groups(w.dv), ps = 1 << a.ps_log2;
+  const int lane = threadIdx.x & 31, part = lane & 3;
+  constexpr int kStep = kThreads / 32;
+  const int per = ((G + kBatch * kStep - 1) / (kBatch * kStep));  // batches of a row
+  for (int it = 0; it < per * (kRows / 8); ++it) {
+    const int g0 = (threadIdx.x >> 5) + it % per * kBatch * kStep;
+    const int r = (lane >> 2) + 8 * (it / per);
+    const int page = sh.page[r], slot = sh.slot[r];
+    // the batch's loads before its first store
+    float x[kBatch][8];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      amax = fmaxf(amax, fabsf(x[j]));
-      finite = finite && fabsf(x[j]) <= FLT_MAX;
+    for (int u = 0; u < kBatch; ++u) {
+      const int gg = g0 + u * kStep;
+      if (page < 0 || gg >= G) continue;
+      const T* src = gg >= gk ? static_cast<const T*>(w.v) + (row0 + r) * w.v_row_stride + (gg - gk) * 32
+                              : static_cast<const T*>(w.k) + (row0 + r) * w.k_row_stride + gg * 32;
+      load8<T, kVec>(src + 8 * part, x[u]);
     }
-    uint32_t code[4] = {0x88888888u, 0x88888888u, 0x88888888u, 0x88888888u};
-    uint32_t byte = 0;
-    if (!finite) {
-      byte = kv4::kNanScale;
-    } else if (amax > 0.f) {
-      const float s = kv4::group_scale(amax);
-      byte = kv4::scale_byte(s);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t word = 0;
+    for (int u = 0; u < kBatch; ++u) {
+      const int gg = g0 + u * kStep;
+      if (gg >= G) break;
+      const bool is_v = gg >= gk;
+      const int g = is_v ? gg - gk : gg, width = is_v ? w.dv : w.dk;
+      // the largest magnitude by its bits, where NaN and infinity come on top
+      uint32_t top = 0u;
+      if (page >= 0) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-          word |= kv4::code_of(x[8 * q + e], s) << (4 * (e >> 1) + 16 * (e & 1));
-        code[q] = word;
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(x[u][j]) & 0x7fffffffu);
       }
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+      top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+      if (page < 0) continue;
+      uint32_t word = 0x88888888u, byte = 0u;
+      if (top >= 0x7f800000u) {
+        byte = kv4::kNanScale;
+      } else if (top != 0u) {
+        const float amax = __uint_as_float(top);
+        const float s = kv4::group_scale(amax), inv = __frcp_rn(s);
+        byte = kv4::scale_byte(s);
+        if (amax > 7.f * s) {  // past the largest scale
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[u][j] = fminf(fmaxf(x[u][j], -7.f * s), 7.f * s);
+        }
+        word = kv4::code_word(x[u], s, inv);
+      }
+      uint8_t* pg = static_cast<uint8_t*>(is_v ? w.v_cache : w.k_cache) +
+                    (int64_t)page * kv4::page_bytes(width, ps);
+      *reinterpret_cast<uint32_t*>(pg + kv4::code_off(g, slot, ps) + 4 * part) = word;
+      if (part == 0) pg[kv4::scale_off(g, slot, ps, kv4::groups(width))] = (uint8_t)byte;
     }
-    uint8_t* pg = static_cast<uint8_t*>(is_v ? w.v_cache : w.k_cache) +
-                  (int64_t)page * kv4::page_bytes(is_v ? w.dv : w.dk, ps);
-    *reinterpret_cast<uint4*>(pg + kv4::code_off(g, slot, ps)) =
-        make_uint4(code[0], code[1], code[2], code[3]);
-    pg[kv4::scale_off(g, slot, ps, is_v ? gv : gk)] = (uint8_t)byte;
   }
 }
 
-template <typename T, bool kVec>
+template <typename T, bool kVec, int kRows>
 __global__ void __launch_bounds__(kThreads)
 kv4_read_kernel(const Kv4Rows a, const uint8_t* __restrict__ cache, int width, T* out,
                 int64_t out_row_stride) {
+  __shared__ Rows<kRows> sh;
+  const int64_t row0 = (int64_t)blockIdx.x * kRows;
+  locate_rows(a, row0, sh);
   const int G = kv4::groups(width), ps = 1 << a.ps_log2;
-  const int64_t total = (int64_t)a.total_tokens * G;
-  for (int64_t it = (int64_t)blockIdx.x * kThreads + threadIdx.x; it < total;
-       it += (int64_t)gridDim.x * kThreads) {
-    const int64_t i = it / G;
-    const int g = (int)(it - i * G);
-    int page, slot;
-    if (!locate(a, i, page, slot)) continue;
+  const int lane = threadIdx.x & 31, part = lane & 3;
+  constexpr int kStep = kThreads / 32;
+  const int per = ((G + kBatch * kStep - 1) / (kBatch * kStep));  // batches of a row
+  for (int it = 0; it < per * (kRows / 8); ++it) {
+    const int g0 = (threadIdx.x >> 5) + it % per * kBatch * kStep;
+    const int r = (lane >> 2) + 8 * (it / per);
+    const int page = sh.page[r], slot = sh.slot[r];
+    if (page < 0) continue;
     const uint8_t* pg = cache + (int64_t)page * kv4::page_bytes(width, ps);
-    const uint4 c = *reinterpret_cast<const uint4*>(pg + kv4::code_off(g, slot, ps));
-    const float s = kv4::scale_value(pg[kv4::scale_off(g, slot, ps, G)]);
-    const uint32_t word[4] = {c.x, c.y, c.z, c.w};
-    T v[32];
+    uint32_t word[kBatch], byte[kBatch];
 #pragma unroll
-    for (int j = 0; j < 32; ++j) {
-      const int e = j & 7;
-      const int n = (int)((word[j >> 3] >> (4 * (e >> 1) + 16 * (e & 1))) & 15u) - 8;
-      v[j] = from_f32<T>((float)n * s);  // exact in bf16 and fp32
+    for (int u = 0; u < kBatch; ++u) {
+      const int g = g0 + u * kStep;
+      if (g >= G) continue;
+      word[u] = __ldg(reinterpret_cast<const uint32_t*>(pg + kv4::code_off(g, slot, ps) + 4 * part));
+      byte[u] = __ldg(pg + kv4::scale_off(g, slot, ps, G));
     }
-    T* dst = out + i * out_row_stride + g * 32;
-    if (kVec) {
 #pragma unroll
-      for (int u = 0; u < (int)(32 * sizeof(T) / 16); ++u)
-        reinterpret_cast<uint4*>(dst)[u] = reinterpret_cast<const uint4*>(v)[u];
-    } else {
+    for (int u = 0; u < kBatch; ++u) {
+      const int g = g0 + u * kStep;
+      if (g >= G) break;
+      const float s = kv4::scale_value(byte[u]);
+      alignas(16) T v[8];
 #pragma unroll
-      for (int j = 0; j < 32; ++j) dst[j] = v[j];
+      for (int e = 0; e < 8; ++e) {
+        const int n = (int)((word[u] >> (4 * (e >> 1) + 16 * (e & 1))) & 15u) - 8;
+        v[e] = from_f32<T>((float)n * s);  // exact in bf16 and fp32
+      }
+      T* dst = out + (row0 + r) * out_row_stride + g * 32 + 8 * part;
+      if (kVec) {
+#pragma unroll
+        for (int q = 0; q < (int)(8 * sizeof(T) / 16); ++q)
+          reinterpret_cast<uint4*>(dst)[q] = reinterpret_cast<const uint4*>(v)[q];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dst[e] = v[e];
+      }
     }
   }
 }
 
-int grid_for(int64_t items) {
-  const int64_t blocks = (items + kThreads - 1) / kThreads;
-  return (int)(blocks < 148 * 16 ? blocks : 148 * 16);
-}
+// Rows of a block: 32 once that still gives every SM blocks for more than one
+// round (the look-up at a block's start is a chain of loads), else 8.
+bool many_rows(int64_t rows) { return rows >= 148 * 64; }
+unsigned grid_for(int64_t rows) { return (unsigned)((rows + (many_rows(rows) ? 31 : 7)) / (many_rows(rows) ? 32 : 8)); }
 
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
 template <typename T>
 cudaError_t append_typed(const Kv4Rows& a, const Kv4Append& w, cudaStream_t s) {
-  const int64_t items = (int64_t)a.total_tokens * (kv4::groups(w.dk) + kv4::groups(w.dv));
   constexpr int kPer = 16 / sizeof(T);
   const bool vec = aligned16(w.k) && w.k_row_stride % kPer == 0 &&
                    (w.dv == 0 || (aligned16(w.v) && w.v_row_stride % kPer == 0));
-  if (vec) kv4_append_kernel<T, true><<<grid_for(items), kThreads, 0, s>>>(a, w);
-  else kv4_append_kernel<T, false><<<grid_for(items), kThreads, 0, s>>>(a, w);
+  const bool many = many_rows(a.total_tokens);
+  auto kern = vec ? (many ? kv4_append_kernel<T, true, 32> : kv4_append_kernel<T, true, 8>)
+                  : (many ? kv4_append_kernel<T, false, 32> : kv4_append_kernel<T, false, 8>);
+  kern<<<grid_for(a.total_tokens), kThreads, 0, s>>>(a, w);
   return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t read_typed(const Kv4Rows& a, const void* cache, int width, void* out, int64_t ors,
                        cudaStream_t s) {
-  const int64_t items = (int64_t)a.total_tokens * kv4::groups(width);
   const bool vec = aligned16(out) && ors % (16 / (int)sizeof(T)) == 0;
   const uint8_t* c = static_cast<const uint8_t*>(cache);
   T* o = static_cast<T*>(out);
-  if (vec) kv4_read_kernel<T, true><<<grid_for(items), kThreads, 0, s>>>(a, c, width, o, ors);
-  else kv4_read_kernel<T, false><<<grid_for(items), kThreads, 0, s>>>(a, c, width, o, ors);
+  const bool many = many_rows(a.total_tokens);
+  auto kern = vec ? (many ? kv4_read_kernel<T, true, 32> : kv4_read_kernel<T, true, 8>)
+                  : (many ? kv4_read_kernel<T, false, 32> : kv4_read_kernel<T, false, 8>);
+  kern<<<grid_for(a.total_tokens), kThreads, 0, s>>>(a, c, width, o, ors);
   return cudaGetLastError();
 }
 

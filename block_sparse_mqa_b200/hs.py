@@ -12,6 +12,7 @@ Function names match the C entry points.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -475,10 +476,40 @@ def hs_swa_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, out, lse, 
     return g
 
 
-def _same_device(*ts):
-    _need_cuda(*ts)
-    if len({t.device for t in ts if t is not None}) > 1:
-        raise ValueError("all tensors must be on one device")
+# The calls below serve single tokens too, where the binding's own time counts:
+# they hand integers to ctypes, ask for the stream's handle alone and change the
+# device only where it is another one.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _same_device(first, *rest):
+    """Device index of the tensors (None is skipped)."""
+    if not first.is_cuda:
+        raise ValueError("all tensors must be CUDA tensors (libhs has no CPU path)")
+    index = first.get_device()
+    for t in rest:
+        if t is not None and (not t.is_cuda or t.get_device() != index):
+            _need_cuda(t)
+            raise ValueError("all tensors must be on one device")
+    return index
+
+
+def _call(fn, index, *args):
+    """fn(*args, stream) on device `index`, on its current stream."""
+    def go():
+        return fn(*args, _raw_stream(index) if _raw_stream else
+                  torch.cuda.current_stream(index).cuda_stream)
+    if torch.cuda.current_device() == index:
+        st = go()
+    else:
+        with torch.cuda.device(index):
+            st = go()
+    if st != HS_OK:
+        _check(st)
 
 
 def _int32(name, t, dims=1):
@@ -504,8 +535,10 @@ def _q_strides(q):
     if q.dim() != 3 or q.stride(2) != 1:
         raise ValueError("q must be [T, H, Dk] with a contiguous last dimension")
     T, H, Dk = q.shape
-    qhs = q.stride(1) if H > 1 else max(q.stride(1), Dk)
-    return (q.stride(0) if T > 1 else max(q.stride(0), H * qhs)), qhs
+    qrs, qhs, _ = q.stride()
+    if H == 1:
+        qhs = max(qhs, Dk)
+    return (qrs if T > 1 else max(qrs, H * qhs)), qhs
 
 
 def _out(name, t, shape, dtype):
@@ -519,7 +552,7 @@ def _sink_ok(sink, H):
 
 
 def _swa_first_check(q, k, v, cu_seqlens, sink, *more):
-    _same_device(q, k, v, cu_seqlens, sink, *more)
+    index = _same_device(q, k, v, cu_seqlens, sink, *more)
     if q.dim() != 3:
         raise ValueError("q must be [T, H, Dk]")
     T, H, Dk = q.shape
@@ -529,27 +562,24 @@ def _swa_first_check(q, k, v, cu_seqlens, sink, *more):
         raise ValueError("k must be [T, Dk]")
     _int32("cu_seqlens", cu_seqlens)
     _sink_ok(sink, H)
-    return T, H, Dk, v.shape[1]
+    return index, T, H, Dk, v.shape[1]
 
 
 def hs_swa_first_mqa_fwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_first: int,
                          sink=None, softmax_scale: float = 0.0, out=None, lse=None):
     """Step 4 with the first num_first tokens of each document always visible.
     Returns (out [T,H,Dv] in q's dtype, lse [T,H] f32)."""
-    T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse)
+    index, T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse)
     qrs, qhs = _q_strides(q)
     o, l = _attn_out(q, v, out, lse)
     _out("out", o, (T, H, Dv), q.dtype)
     _out("lse", l, (T, H), torch.float32)
     if T == 0:
         return o, l
-    with torch.cuda.device(q.device):
-        _check(lib().hs_swa_first_mqa_fwd(
-            _ptr(q), qrs, qhs, _ptr(k), _row_stride(k), _ptr(v), _row_stride(v),
-            _ptr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen), H, Dk, Dv,
-            _dtype_code(q), float(softmax_scale), int(window), int(num_first), _ptr(sink),
-            _ptr(o), _ptr(l),
-            _stream(q.device)))
+    _call(lib().hs_swa_first_mqa_fwd, index, _addr(q), qrs, qhs, _addr(k), _row_stride(k),
+          _addr(v), _row_stride(v), _addr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen),
+          H, Dk, Dv, _dtype_code(q), float(softmax_scale), int(window), int(num_first),
+          _addr(sink), _addr(o), _addr(l))
     return o, l
 
 
@@ -558,8 +588,8 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
                          workspace=None):
     """Backward of hs_swa_first_mqa_fwd.  Returns (dq [T,H,Dk], dk [T,Dk], dv [T,Dv])
     in q's dtype and dsink [H] float32 (None without a sink)."""
-    T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse, dout, workspace,
-                                    *(grads or ()))
+    index, T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse, dout, workspace,
+                                           *(grads or ()))
     qrs, qhs = _q_strides(q)
     _out("out", out, (T, H, Dv), q.dtype)
     _out("dout", dout, (T, H, Dv), q.dtype)
@@ -581,16 +611,15 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
         workspace = torch.empty(workspace_size(HS_OP_SWA_FIRST_MQA_BWD, T, nd, max_seqlen, H, Dk,
                                                Dv, q.dtype, span),
                                 device=q.device, dtype=torch.uint8)
-    with torch.cuda.device(q.device):
-        _check(lib().hs_swa_first_mqa_bwd(
-            _ptr(q), qrs, qhs, _ptr(k), _row_stride(k), _ptr(v), _row_stride(v),
-            _ptr(cu_seqlens), nd, T, int(max_seqlen), H, Dk, Dv, _dtype_code(q),
-            float(softmax_scale), int(window), int(num_first), _ptr(sink), _ptr(out), _ptr(lse), _ptr(dout), _ptr(grads[0]),
-            _ptr(grads[1]), _ptr(grads[2]), _ptr(grads[3]), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(q.device)))
+    _call(lib().hs_swa_first_mqa_bwd, index, _addr(q), qrs, qhs, _addr(k), _row_stride(k),
+          _addr(v), _row_stride(v), _addr(cu_seqlens), nd, T, int(max_seqlen), H, Dk, Dv,
+          _dtype_code(q), float(softmax_scale), int(window), int(num_first), _addr(sink),
+          _addr(out), _addr(lse), _addr(dout), _addr(grads[0]), _addr(grads[1]), _addr(grads[2]),
+          _addr(grads[3]), _addr(workspace), workspace.numel() * workspace.element_size())
     return grads
 
 
+@functools.lru_cache(maxsize=256)
 def kv4_page_bytes(width: int, page_size: int) -> int:
     """Bytes of one page of a 4-bit cache plane (ValueError if unsupported)."""
     n = int(lib().hs_kv4_page_bytes(int(width), int(page_size)))
@@ -607,7 +636,7 @@ def kv4_cache(num_pages: int, width: int, page_size: int, device="cuda"):
 
 
 def _plane(name, cache, width, page_size, like=None):
-    if cache.dtype != torch.uint8 or not cache.is_contiguous() or cache.dim() != 2 or \
+    if cache.dtype != torch.uint8 or cache.dim() != 2 or not cache.is_contiguous() or \
             cache.shape[1] != kv4_page_bytes(width, page_size):
         raise ValueError("%s must be contiguous uint8 [num_pages, %d] (width %d, page size %d)"
                          % (name, kv4_page_bytes(width, page_size), width, page_size))
@@ -622,14 +651,14 @@ def _table_args(block_table, seq_lens, num_pages, page_size):
         raise ValueError("block_table must have one row per sequence")
     # a single row's stride may be anything; the library wants at least the width
     stride = max(block_table.stride(0), block_table.shape[1])
-    return _ptr(block_table), stride, block_table.shape[1], num_pages, int(page_size)
+    return _addr(block_table), stride, block_table.shape[1], num_pages, int(page_size)
 
 
 def hs_kv4_append(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens, page_size: int):
     """Quantise the packed rows k [T,Dk] (and v [T,Dv], or None with v_cache None)
     to 4 bits and write them behind the rows their sequences already have;
     seq_lens counts the new rows too (see include/hs.h)."""
-    _same_device(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens)
+    index = _same_device(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens)
     if (v is None) != (v_cache is None):
         raise ValueError("v and v_cache go together")
     _rows("k", k, None)
@@ -644,11 +673,10 @@ def hs_kv4_append(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens, pag
     table = _table_args(block_table, seq_lens, k_cache.shape[0], page_size)
     if T == 0:
         return
-    with torch.cuda.device(k.device):
-        _check(lib().hs_kv4_append(
-            _ptr(k), _row_stride(k), _ptr(v), 0 if v is None else _row_stride(v), _ptr(k_cache),
-            _ptr(v_cache), *table, _ptr(cu_seqlens), _ptr(seq_lens), seq_lens.numel(), T,
-            k.shape[1], 0 if v is None else v.shape[1], _dtype_code(k), _stream(k.device)))
+    _call(lib().hs_kv4_append, index, _addr(k), _row_stride(k), _addr(v),
+          0 if v is None else _row_stride(v), _addr(k_cache), _addr(v_cache), *table,
+          _addr(cu_seqlens), _addr(seq_lens), seq_lens.numel(), T, k.shape[1],
+          0 if v is None else v.shape[1], _dtype_code(k))
 
 
 def hs_kv4_read(cache, width: int, block_table, cu_seqlens, seq_lens, page_size: int,
@@ -656,7 +684,7 @@ def hs_kv4_read(cache, width: int, block_table, cu_seqlens, seq_lens, page_size:
     """The values of the last rows of each sequence (as many as cu_seqlens has for
     it), packed: [total_tokens, width].  Rows behind the last sequence are left
     as they are (unset in a new tensor)."""
-    _same_device(cache, block_table, cu_seqlens, seq_lens, out)
+    index = _same_device(cache, block_table, cu_seqlens, seq_lens, out)
     _plane("cache", cache, width, page_size)
     _int32("cu_seqlens", cu_seqlens)
     if cu_seqlens.numel() != seq_lens.numel() + 1:
@@ -669,10 +697,9 @@ def hs_kv4_read(cache, width: int, block_table, cu_seqlens, seq_lens, page_size:
         raise ValueError("out must be [total_tokens, width]")
     if total_tokens == 0:
         return o
-    with torch.cuda.device(cache.device):
-        _check(lib().hs_kv4_read(
-            _ptr(cache), int(width), *table, _ptr(cu_seqlens), _ptr(seq_lens), seq_lens.numel(),
-            int(total_tokens), _ptr(o), _row_stride(o), _dtype_code(o), _stream(cache.device)))
+    _call(lib().hs_kv4_read, index, _addr(cache), int(width), *table, _addr(cu_seqlens),
+          _addr(seq_lens), seq_lens.numel(), int(total_tokens), _addr(o), _row_stride(o),
+          _dtype_code(o))
     return o
 
 
@@ -683,7 +710,7 @@ def hs_kv4_mqa_decode(q, k_cache, v_cache, block_table, seq_lens, max_seqlen: in
     the first dv columns of the keys); window 0 attends everything, else the
     first num_first tokens and the last `window`.  Returns (out [S,H,dv] in
     q's dtype, lse [S,H] f32)."""
-    _same_device(q, k_cache, v_cache, block_table, seq_lens, sink, out, lse, workspace)
+    index = _same_device(q, k_cache, v_cache, block_table, seq_lens, sink, out, lse, workspace)
     qrs, qhs = _q_strides(q)
     S, H, Dk = q.shape
     if seq_lens.numel() != S:
@@ -703,12 +730,10 @@ def hs_kv4_mqa_decode(q, k_cache, v_cache, block_table, seq_lens, max_seqlen: in
         workspace = torch.empty(workspace_size(HS_OP_KV4_MQA_DECODE, S, S, max_seqlen, H, Dk, dv,
                                                q.dtype, page_size),
                                 device=q.device, dtype=torch.uint8)
-    with torch.cuda.device(q.device):
-        _check(lib().hs_kv4_mqa_decode(
-            _ptr(q), qrs, qhs, _ptr(k_cache), _ptr(v_cache), *table, _ptr(seq_lens), S,
-            int(max_seqlen), H, Dk, int(dv), _dtype_code(q), float(softmax_scale), int(window),
-            int(num_first), _ptr(sink), _ptr(o), _ptr(l), _ptr(workspace),
-            workspace.numel() * workspace.element_size(), _stream(q.device)))
+    _call(lib().hs_kv4_mqa_decode, index, _addr(q), qrs, qhs, _addr(k_cache), _addr(v_cache),
+          *table, _addr(seq_lens), S, int(max_seqlen), H, Dk, int(dv), _dtype_code(q),
+          float(softmax_scale), int(window), int(num_first), _addr(sink), _addr(o), _addr(l),
+          _addr(workspace), workspace.numel() * workspace.element_size())
     return o, l
 
 
