@@ -11,9 +11,9 @@
 // key's (token, head) pairs as the summed dimension; p and ds serve both, so
 // they are computed once, in the query-major pass, and written as bf16 (the
 // rounding the products need anyway) into a band in the workspace:
-//   band[t][h][c] is key base(t) + c, base(t) = (t & ~7) - Wp, c < Wp + 8
-// (Wp: window - 1 up to a multiple of 8), and behind it the first tokens'
-// columns, key bos + c.  Everything outside a token's key set is written as 0.
+//   band[t][h][c] is key base(t) + c, base(t) = (t & ~7) - Wp, c < bw
+// (Wp: window - 1 up to a multiple of 8; bw: Wp + 8 up to one of 16), and behind
+// it the first tokens' columns, key bos + c - bw.  Everything outside a token's key set is written as 0.
 // The key-major pass is then a plain product over the band: a tile's 256 keys
 // are columns base-shifted per token, which a TMA box fetches for any token;
 // columns left or right of the band read as 0, so documents and window edges
@@ -87,48 +87,45 @@ constexpr size_t kSmem = (size_t)2 * kSlots * kSlot + (size_t)(kMaxQC + kMaxDC) 
                          4 * kStage + sizeof(Shared);
 static_assert(kSmem <= 232448, "shared memory of one CTA");
 
-// The tiles of a pass: window columns first, then the first tokens'.
+// The tiles of a pass: 128 columns of the band each, the window's before the
+// first tokens'.
 struct Tiles {
-  int key0w, ntw, ntf;  // key of window column 0; tiles of the two regions
-  int lo, hi;           // keys some token of the pass sees in its window
-  int nf;               // first tokens some token of the pass sees
-  int bw, fp, bos;
+  int key0, bw, cols, bos;  // key of column 0; the window's and all columns
+  int lo, hi;               // keys some token of the pass sees in its window
+  int nf;                   // first tokens some token of the pass sees
   __device__ __forceinline__ Tiles(const Pass& ps, const Band& b) {
     const int last = ps.t0 + (ps.mode == 2 ? 1 : 0);
-    key0w = (ps.t0 & ~7) - b.wp;
+    key0 = (ps.t0 & ~7) - b.wp;
     bw = b.bw;
-    fp = b.fp;
+    cols = b.bw + b.fp;
     bos = ps.bos;
-    ntw = (bw + 127) / 128;
-    ntf = (fp + 127) / 128;
     lo = ps.wlo;
     hi = last;
     nf = min(b.first, max(bos, last - b.window + 1) - bos);
   }
-  __device__ __forceinline__ int count() const { return ntw + ntf; }
-  __device__ __forceinline__ int col0(int i) const { return i < ntw ? 128 * i : 128 * (i - ntw); }
-  __device__ __forceinline__ int cols(int i) const {  // stored columns, a multiple of 8
-    return min(128, (i < ntw ? bw : fp) - col0(i));
-  }
-  __device__ __forceinline__ int n(int i) const { return (cols(i) + 31) & ~31; }
-  __device__ __forceinline__ int key0(int i) const { return (i < ntw ? key0w : bos) + col0(i); }
+  __device__ __forceinline__ int count() const { return (cols + 127) / 128; }
+  __device__ __forceinline__ int n(int i) const { return (min(128, cols - 128 * i) + 31) & ~31; }
   __device__ __forceinline__ bool live(int i) const {
-    return i < ntw ? key0(i) <= hi && key0(i) + n(i) > lo : col0(i) < nf;
+    const int c0 = 128 * i, c1 = c0 + n(i);
+    return (c0 < bw && key0 + c0 <= hi && key0 + min(c1, bw) > lo) ||
+           (c1 > bw && max(c0, bw) - bw < nf);
   }
+  // Row of the 16 columns from c (a multiple of 16).
+  __device__ __forceinline__ int row(int c) const { return c < bw ? key0 + c : bos + (c - bw); }
 };
 
-// `rows` consecutive rows (a multiple of 16) from `row`, `cnt` 64-column
-// chunks `pitch` bytes apart.
-__device__ __forceinline__ void load_block(const CUtensorMap* big, const CUtensorMap* small,
-                                           uint8_t* dst, uint32_t bar, int row, int rows, int col,
-                                           int cnt, int pitch, int lane) {
-  if (rows == 64) {
-    if (lane < cnt) tma_pair_2d(dst + lane * pitch, big, bar, col + 64 * lane, row);
+// The keys of `rows` columns (a multiple of 16) from column c, `cnt` 64-column
+// chunks of K or V `pitch` bytes apart.
+__device__ __forceinline__ void load_block(const Tiles& tl, const CUtensorMap* big,
+                                           const CUtensorMap* small, uint8_t* dst, uint32_t bar,
+                                           int c, int rows, int col, int cnt, int pitch, int lane) {
+  if (rows == 64 && c + 64 <= tl.bw) {
+    if (lane < cnt) tma_pair_2d(dst + lane * pitch, big, bar, col + 64 * lane, tl.row(c));
   } else {
     const int boxes = rows / 16;
     for (int e = lane; e < boxes * cnt; e += 32) {
-      const int c = e / boxes, bx = e - c * boxes;
-      tma_pair_2d(dst + c * pitch + bx * 2048, small, bar, col + 64 * c, row + 16 * bx);
+      const int q = e / boxes, bx = e - q * boxes;
+      tma_pair_2d(dst + q * pitch + bx * 2048, small, bar, col + 64 * q, tl.row(c + 16 * bx));
     }
   }
   __syncwarp();
@@ -238,9 +235,9 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           tell_leader(&sh->sempty[buf]);
           tell_leader(&sh->dpempty);
           if (mine) {
-            const int s0 = tl.key0(i) + k0;
-            const uint32_t bits = (i < tl.ntw ? range_bits(own - s0, t - s0)
-                                              : range_bits(0, nf - 1 - (s0 - ps.bos))) &
+            const int s0 = 128 * i + k0;  // band column
+            const uint32_t bits = (range_bits(own - tl.key0 - s0, t - tl.key0 - s0) |
+                                   range_bits(tl.bw - s0, tl.bw + nf - 1 - s0)) &
                                   low_bits(n2 - c0);
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
@@ -273,8 +270,8 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
           tell_leader(&sh->dsfull);
         }
         if (mine) {
-          const int64_t at = th * p.band.stride + (i < tl.ntw ? 0 : tl.bw) + tl.col0(i) + k0;
-          const int left = tl.cols(i) - k0;
+          const int64_t at = th * p.band.stride + 128 * i + k0;
+          const int left = tl.cols - 128 * i - k0;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
             if (8 * q >= left || c0 + 8 * q >= n2) break;
@@ -333,7 +330,7 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         }
         for (int i = 0; i < tl.count() && ok; ++i) {
           if (!tl.live(i)) continue;
-          const int n = tl.n(i), key = tl.key0(i);
+          const int n = tl.n(i);
           if (!two) {  // K, then V: this CTA's half of the keys
             const int rows = n / 2, per = 128 / rows;
             for (int v = 0; v < 2 && ok; ++v) {
@@ -341,8 +338,8 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               for (int c = 0; c < nch && ok; c += per, next()) {
                 const int cnt = min(per, nch - c);
                 if (!claim(cnt * rows * 128)) { ok = false; break; }
-                load_block(v ? &vmap : &kmap, v ? &vmap16 : &kmap16, ring + slot * kSlot,
-                           leader_addr(&fullb[slot]), key + rank * rows, rows, c * 64, cnt,
+                load_block(tl, v ? &vmap : &kmap, v ? &vmap16 : &kmap16, ring + slot * kSlot,
+                           leader_addr(&fullb[slot]), 128 * i + rank * rows, rows, c * 64, cnt,
                            rows * 128, lane);
               }
             }
@@ -352,8 +349,8 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
               for (int k0 = 0; k0 < n && ok; k0 += 64, next()) {
                 const int rows = min(64, n - k0);
                 if (!claim(rows * 128 * panels)) { ok = false; break; }
-                load_block(&kmap, &kmap16, ring + slot * kSlot, leader_addr(&fullb[slot]), key + k0,
-                           rows, col, panels, 8192, lane);
+                load_block(tl, &kmap, &kmap16, ring + slot * kSlot, leader_addr(&fullb[slot]),
+                           128 * i + k0, rows, col, panels, 8192, lane);
               }
             }
           }
@@ -572,8 +569,13 @@ struct Jobs {
     const int total = nwin + (p.band.fp > 0 ? p.chunks * p.groups : 0);
     const int W = p.dk + p.dv;
     for (; item < total; item += step) {
+      // group-major: items that run together share q or dout, and the wide
+      // columns come before a last, narrow group of Dv or Dk
       const int e = item < nwin ? item : item - nwin;
-      const int g = e % p.groups, r = e / p.groups;
+      const int per = item < nwin ? p.tiles * p.parts : p.chunks;
+      int g = e / per;
+      const int r = e - g * per;
+      g = g < p.groups - p.gk ? p.gk + g : g - (p.groups - p.gk);
       j.is_k = g < p.gk;
       const int gi = j.is_k ? g : g - p.gk;
       j.col0 = 512 * gi;
@@ -825,9 +827,9 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
 
 size_t align256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Row stride of the band for a window and first tokens of together `span`
-// keys: window - 1 and first up to multiples of 8, and 8 more.
-int64_t band_stride(int64_t span) { return (span + 23) & ~(int64_t)7; }
+// Row stride of the band, at least bw + fp, for a window and first tokens of
+// together `span` keys.
+int64_t band_stride(int64_t span) { return (span + 51) & ~(int64_t)7; }
 
 struct Sizes {
   size_t band, wpart, fpart;
@@ -854,7 +856,7 @@ size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, in
   if (span < 1) span = 1;
   if (span > 2 * max_seqlen) span = 2 * max_seqlen;
   // the most any split of the span into window and first tokens needs
-  const int fp = std::min((span + 7) & ~7, pb::kKeys);
+  const int fp = std::min((span + 15) & ~15, pb::kKeys);
   const Sizes z = sizes_of(total_tokens, num_docs, span, std::min(span, max_seqlen), fp, dk, dv);
   const size_t n = 2 * z.band + z.wpart + z.fpart;
   return n <= kMostBytes ? n : 0;
@@ -869,8 +871,8 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   // a window that holds every document leaves no first token outside
   band.first = band.window >= p.max_seqlen ? 0 : std::min(b.first, p.max_seqlen);
   band.wp = (band.window - 1 + 7) & ~7;
-  band.bw = band.wp + 8;
-  band.fp = (band.first + 7) & ~7;
+  band.bw = (band.wp + 8 + 15) & ~15;
+  band.fp = (band.first + 15) & ~15;
   band.stride = band_stride(band.window + band.first);
   if (band.fp > pb::kKeys) return cudaSuccess;
   const Sizes z = sizes_of(p.total_tokens, p.num_docs, band.window + band.first, band.window,
