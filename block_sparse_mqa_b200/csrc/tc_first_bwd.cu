@@ -20,9 +20,11 @@
 // need no case of their own.
 //   pass A  per pair of tokens, tiles of 128 keys: S = Q K^T, dP = dO V^T,
 //           P and dS to the band, dQ += dS K                   (M = 128)
-//   pass B  per (256 keys, 128 tokens, 512 columns of dk or dv): partial
+//   pass B  per (tok tokens, 256 keys, 512 columns of dk or dv): partial
 //           dV^T += dO^T P or dK^T += Q^T dS                   (M = 256, N = 256)
-//           and the same per (128 tokens of a document, its first tokens)
+//           and the same per (tok tokens of a document, its first tokens).
+//           Items go by their tokens, so that the ones running together read
+//           the same q and dout from L2 (each token meets three key tiles).
 //   reduce  adds a key's partial sums in order, scales, rounds once
 // Results are deterministic.  All waits are bounded (HS_ERR_TIMEOUT).
 
@@ -524,7 +526,8 @@ namespace pb {
 
 constexpr int kThreads = 256;   // warp 0 producer, warp 1 issuer, warps 4..7 epilogue
 constexpr int kKeys = 256;      // keys of a window item
-constexpr int kTok = 128;       // tokens of an item
+// Tokens of an item: many make few partial sums, few keep every SM busy.
+__host__ __device__ constexpr int tok_of(int T) { return T >= 2048 ? 128 : T >= 1024 ? 64 : 32; }
 constexpr int kStages = 4;
 constexpr int kPanel = 8192;    // 64 heads x 64 columns
 constexpr int kStageBytes = 6 * kPanel;  // 4 panels of q or dout, 2 of the band
@@ -535,7 +538,7 @@ struct Params {
   int dk, dv;
   int gk, groups;     // 512-column groups of Dk; of Dk and Dv together
   int tiles, parts;   // key tiles; token parts of a tile
-  int chunks;         // kTok-token chunks of the whole batch
+  int tok, chunks;    // tokens of an item; as many chunks of them in the batch
   float* wpart;       // [tiles][parts][kKeys][dk + dv]
   float* fpart;       // [chunks + num_docs][fp][dk + dv]
   int* status;
@@ -565,29 +568,30 @@ struct Jobs {
   __device__ __forceinline__ Jobs(const Params& pp, int first, int pairs)
       : p(pp), item(first), step(pairs), doc_t(-1) {}
   __device__ __forceinline__ bool next(Job& j) {
-    const int nwin = p.tiles * p.parts * p.groups;
+    // chunk by chunk of tokens: the key tiles it meets (from its own backwards),
+    // the column groups of each
+    const int per = kKeys / p.tok, meets = (p.parts + per - 1) / per;
+    const int nwin = p.chunks * meets * p.groups;
     const int total = nwin + (p.band.fp > 0 ? p.chunks * p.groups : 0);
     const int W = p.dk + p.dv;
     for (; item < total; item += step) {
-      // group-major: items that run together share q or dout, and the wide
-      // columns come before a last, narrow group of Dv or Dk
       const int e = item < nwin ? item : item - nwin;
-      const int per = item < nwin ? p.tiles * p.parts : p.chunks;
-      int g = e / per;
-      const int r = e - g * per;
-      g = g < p.groups - p.gk ? p.gk + g : g - (p.groups - p.gk);
+      const int g = e % p.groups;
+      int r = e / p.groups;
       j.is_k = g < p.gk;
       const int gi = j.is_k ? g : g - p.gk;
       j.col0 = 512 * gi;
       j.cols = min(512, (j.is_k ? p.dk : p.dv) - j.col0);
       const int at = (j.is_k ? 0 : p.dk) + j.col0;
       if (item < nwin) {
-        const int tile = r / p.parts, part = r - tile * p.parts;
+        const int chunk = r / meets, tile = chunk / per - r % meets, part = chunk - tile * per;
+        if (tile < 0 || part >= p.parts) continue;
+        r = tile * p.parts + part;
         j.window = true;
         j.key0 = tile * kKeys;
         j.n = kKeys;
-        j.t0 = j.key0 + part * kTok;
-        j.t1 = min(min(j.t0 + kTok, p.d.T), j.key0 + kKeys - 1 + p.band.window);
+        j.t0 = chunk * p.tok;
+        j.t1 = min(min(j.t0 + p.tok, p.d.T), j.key0 + kKeys - 1 + p.band.window);
         if (j.t0 >= j.t1) continue;
         j.dst = p.wpart + (int64_t)r * kKeys * W + at;
         j.keys = min(kKeys, p.d.T - j.key0);
@@ -595,7 +599,7 @@ struct Jobs {
         return true;
       }
       // a chunk of tokens: its documents one after the other
-      const int c0 = r * kTok, c1 = min(p.d.T, c0 + kTok);
+      const int c0 = r * p.tok, c1 = min(p.d.T, c0 + p.tok);
       for (int t = doc_t < 0 ? c0 : doc_t; t < c1;) {
         int lo = 0, hi = p.d.num_docs;
         while (hi - lo > 1) {
@@ -784,7 +788,7 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
   for (int j = blockIdx.x; j < p.d.T; j += gridDim.x) {
     const int tile = j / kKeys, key0 = tile * kKeys;
     const int tend = min(p.d.T, key0 + kKeys - 1 + p.band.window);
-    const int parts = min(p.parts, (tend - key0 + kTok - 1) / kTok);
+    const int parts = min(p.parts, (tend - key0 + p.tok - 1) / p.tok);
     int bos, eos, doc = 0, c0 = 1, c1 = 0, f = 0;  // chunks with first-token sums
     if (p.band.fp > 0 &&
         find_doc(p.d.cu, p.d.num_docs, p.d.T, p.d.max_seqlen, j, bos, eos, nullptr)) {
@@ -796,8 +800,8 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
           if (__ldg(p.d.cu + mid) <= j) lo = mid; else hi = mid;
         }
         doc = lo;
-        c0 = (bos + p.band.window) / kTok;
-        c1 = (eos - 1) / kTok;
+        c0 = (bos + p.band.window) / p.tok;
+        c1 = (eos - 1) / p.tok;
       }
     }
     for (int col = threadIdx.x * 4; col < W; col += 1024) {
@@ -840,8 +844,9 @@ Sizes sizes_of(int T, int num_docs, int span, int window, int fp, int dk, int dv
   const size_t W = (size_t)(dk + dv) * sizeof(float);
   z.band = align256((size_t)T * kH * band_stride(span) * 2);
   z.tiles = (T + pb::kKeys - 1) / pb::kKeys;
-  z.parts = (pb::kKeys - 1 + window + pb::kTok - 1) / pb::kTok;
-  z.chunks = (T + pb::kTok - 1) / pb::kTok;
+  const int tok = pb::tok_of(T);
+  z.parts = (pb::kKeys - 1 + window + tok - 1) / tok;
+  z.chunks = (T + tok - 1) / tok;
   z.wpart = align256((size_t)z.tiles * z.parts * pb::kKeys * W);
   z.fpart = align256((size_t)(z.chunks + num_docs) * fp * W);
   return z;
@@ -933,6 +938,7 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   k.groups = k.gk + (p.dv + 511) / 512;
   k.tiles = z.tiles;
   k.parts = z.parts;
+  k.tok = pb::tok_of(T);
   k.chunks = z.chunks;
   k.wpart = reinterpret_cast<float*>(w + 2 * z.band);
   k.fpart = reinterpret_cast<float*>(w + 2 * z.band + z.wpart);
