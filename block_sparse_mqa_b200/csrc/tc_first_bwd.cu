@@ -311,25 +311,21 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       };
       while (ok && walk.next(ps, leader && !two ? p.status : nullptr)) {
         const Tiles tl(ps, p.band);
-        if (!two) {  // Q and dO chunks, each once the pass before has read it
-          for (int c = 0; c < p.nck + p.ndc && ok; ++c) {
-            const bool q = c < p.nck;
-            const int e = q ? c : c - p.nck;
-            uint64_t* const full = q ? &sh->qfull[e] : &sh->dfull[e];
-            if (!first_pass && !warp_wait(q ? &sh->qempty[e] : &sh->dempty[e], qph ^ 1, lim)) {
-              ok = false;
-              break;
-            }
-            if (lane == 0) {
-              if (leader) mbar_expect_tx(full, 2 * kQChunk);
-              tma_pair_3d((q ? qbuf : dbuf) + e * kQChunk, q ? &qmap : &dmap, leader_addr(full),
-                          e * 64, 0, ps.token(rank));
-            }
-            __syncwarp();
+        // Q (with K and V) and dO (with K's columns, which the tile needs last)
+        // chunk by chunk, each once the pass before has read it
+        uint64_t* const mfull = two ? sh->dfull : sh->qfull;
+        uint64_t* const mempty = two ? sh->dempty : sh->qempty;
+        for (int c = 0; c < (two ? p.ndc : p.nck) && ok; ++c) {
+          if (!first_pass && !warp_wait(&mempty[c], qph ^ 1, lim)) { ok = false; break; }
+          if (lane == 0) {
+            if (leader) mbar_expect_tx(&mfull[c], 2 * kQChunk);
+            tma_pair_3d((two ? dbuf : qbuf) + c * kQChunk, two ? &dmap : &qmap,
+                        leader_addr(&mfull[c]), c * 64, 0, ps.token(rank));
           }
-          first_pass = false;
-          qph ^= 1;
+          __syncwarp();
         }
+        first_pass = false;
+        qph ^= 1;
         for (int i = 0; i < tl.count() && ok; ++i) {
           if (!tl.live(i)) continue;
           const int n = tl.n(i);
