@@ -25,7 +25,7 @@
 // codes of tile i + 1 wait in registers since before the softmax of tile i.
 // A value plane of its own is expanded into the panels after QK.
 //
-// 8 warps expand and compute the softmax (thread = key row of S^T, 32 heads);
+// 16 warps expand and compute the softmax (thread = key row of S^T, 16 heads);
 // two further warps issue the QK and the PV MMAs.  The running maximum of a
 // head is raised only when a logit passes it by more than 2^8, so a tile
 // usually needs one vote and no reduction.
@@ -48,7 +48,7 @@ namespace {
 
 using namespace tc;
 
-constexpr int kWarps = 8;               // expansion and softmax (16 had 96 registers each, spilled and took 129 us for 106)
+constexpr int kWarps = 16;              // expansion and softmax (8: 88 us for 80)
 constexpr int kParts = kWarps / 4;    // each part of the warps has 64 / kParts heads
 constexpr int kHP = 64 / kParts;
 constexpr int kPE = 8 / kParts;       // panels of a thread
@@ -219,13 +219,23 @@ __device__ __forceinline__ void publish(uint64_t* bar, int lane) {
   if (lane == 0) mbar_arrive(bar);
 }
 
+__device__ __forceinline__ void tmem_ld_heads(uint32_t at, uint32_t (&u)[kHP]) {
+  static_assert(kHP == 16, "the heads of a part");
+  tmem_ld16(at, u);
+}
+
 template <bool kAlias>
 __global__ void __launch_bounds__(kThreads, 1)
 tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* base = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~static_cast<uintptr_t>(1023));
-  uint8_t* const panels = base;
+  // Not aligned by hand: through an integer the compiler loses that the pointer
+  // is into shared memory, and every access below became a generic one with a
+  // 64-bit address (106 us against 88, and 240 registers wanted).
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023) {
+    record_status(p.a.status, HS_ERR_CUDA);
+    return;
+  }
+  uint8_t* const panels = smem_raw;
   uint8_t* const qbuf = panels + p.panels * kPanel;
   uint8_t* const pown = qbuf + p.nck * kQChunk;
   uint8_t* const pbuf = p.own_p ? pown : panels + 8 * kPanel;
@@ -427,7 +437,7 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
         const bool first = i == ta;
         if (act) {
           uint32_t u[kHP];
-          tmem_ld32(lane_base + kSCol + hb, u);
+          tmem_ld_heads(lane_base + kSCol + hb, u);
           tmem_ld_wait();
           reg_fence(u);
           const bool valid = i * kTile + r < kl.n;
@@ -581,7 +591,7 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 #pragma unroll 1
         for (int c = 0; c < p.nvc; ++c) {
           uint32_t w[kHP];
-          tmem_ld32(lane_base + c * kHG + hb, w);
+          tmem_ld_heads(lane_base + c * kHG + hb, w);
           tmem_ld_wait();
           reg_fence(w);
           if (c * 128 + r >= a.dv) continue;
@@ -616,6 +626,7 @@ tc_kv4_decode_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_cons
 // sequences.  One block per (sequence, 8 heads).
 __global__ void __launch_bounds__(256) tc_kv4_join_kernel(const __grid_constant__ Params p) {
   const Kv4Decode& a = p.a;
+  cudaGridDependencySynchronize();  // launched while the decode kernel still runs
   const int b = blockIdx.x, h = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   const int gs = p.prefix[b], ge = p.prefix[b + 1], total = p.prefix[a.num_seqs];
   if (h >= a.num_heads) return;
@@ -748,7 +759,7 @@ cudaError_t launch_tc_kv4_decode(const Kv4Decode& a, long long wait_limit, cudaS
     const uint32_t box[3] = {64, (uint32_t)p.qrows, 1};
     if (!encode_bf16_map(&qmap, a.q, 3, dims, strides, box)) return cudaErrorInvalidValue;
   }
-  const size_t bytes = 1024 + (size_t)p.panels * kPanel + (size_t)p.nck * kQChunk +
+  const size_t bytes = (size_t)p.panels * kPanel + (size_t)p.nck * kQChunk +
                        (p.own_p ? kPBytes : 0) + sizeof(Shared);
   auto kern = a.v_cache ? tc_kv4_decode_kernel<false> : tc_kv4_decode_kernel<true>;
   cudaError_t e =
@@ -757,8 +768,16 @@ cudaError_t launch_tc_kv4_decode(const Kv4Decode& a, long long wait_limit, cudaS
   kern<<<p.ctas * p.groups, kThreads, bytes, s>>>(qmap, p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  tc_kv4_join_kernel<<<dim3(a.num_seqs, (a.num_heads + 7) / 8), 256, 0, s>>>(p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(a.num_seqs, (a.num_heads + 7) / 8);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, tc_kv4_join_kernel, p);
 }
 
 }  // namespace hs
