@@ -610,8 +610,8 @@ static hs_status backward_common(hs::BwdArgs& a, bool sparse, const void* q, int
   r = status_ptr(&a.p.status);
   if (r != HS_OK) return r;
   int path = HS_PATH_SIMT;
-  return launched_on(hs::launch_simt_backward(a, sparse, !g_force_simt.load(), &path, stream),
-                     sparse ? "sparse attention backward" : "swa attention backward", path);
+  const cudaError_t e = hs::launch_simt_backward(a, sparse, !g_force_simt.load(), &path, stream);
+  return launched_on(e, sparse ? "sparse attention backward" : "swa attention backward", path);
 }
 
 hs_status hs_sparse_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_head_stride,
