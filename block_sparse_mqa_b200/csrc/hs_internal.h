@@ -105,8 +105,8 @@ bool tc_first_eligible(const Problem& p);
 // them out.
 size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, int span, int dk,
                               int dv);
-cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled, void* ws,
-                                size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s);
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled,
+                                int* spoiled_keys, void* ws, size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s);
 cudaError_t launch_tc_first_fwd(const AttnArgs& a, long long wait_limit, cudaStream_t s);
 size_t simt_backward_workspace(int total_tokens, int num_heads);
 // *path (may be null) receives the kernel family the dq and dk / dv passes use.
@@ -124,7 +124,8 @@ size_t tc_bwd_dkdv_workspace(int total_tokens, int dk, int dv);
 // `spoiled` (may be null): set to 1 per token whose dq is not finite.
 cudaError_t launch_tc_bwd_dq(const BwdArgs& a, bool sparse, const float* delta, int* spoiled,
                              long long wait_limit, cudaStream_t s);
-cudaError_t launch_tc_bwd_dkdv(const BwdArgs& a, bool sparse, const float* delta,
+// `spoiled` as above, per key whose dk or dv is not finite.
+cudaError_t launch_tc_bwd_dkdv(const BwdArgs& a, bool sparse, const float* delta, int* spoiled,
                                long long wait_limit, cudaStream_t s);
 
 // Shared-memory bytes the CUDA-core block-score kernel needs (0 if it cannot run).

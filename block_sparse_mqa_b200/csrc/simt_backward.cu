@@ -48,11 +48,11 @@ struct BwdParams {
   void* dval;
   float* dsink;
   int first;           // window: first tokens of the document that stay visible
-  bool like_input;
+  bool like_input, with_first;
   float* delta;       // workspace [T, H]
   float* dsink_part;  // workspace [T, H]
   int G, KT;          // heads per group, keys per dq tile
-  const int* only;    // dq of the tokens with only[t] != 0 alone (null: all)
+  const int* only;    // the tokens (or keys) with only[t] != 0 alone (null: all)
 };
 
 template <typename T>
@@ -299,7 +299,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
       }
       // candidate queries t (those whose key set can meet [s0, s1)), in
       // chunks of kThreads: thread i tests t = c0 + i
-      const int tend = kSparse || s0 - bos < a.first ? eos : min(eos, s1 - 1 + a.window);
+      const int tend = kSparse ? eos : min(eos, s1 - 1 + a.window);
       const int ba = kSparse ? (s0 - bos) / a.B : 0, bb = kSparse ? (s1 - 1 - bos) / a.B : 0;
       for (int c0 = s0; c0 < tend; c0 += kThreads) {
         const int t = c0 + tid;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
           } else {
             for (int jj = 0; jj < n; ++jj) {
               const int j = s0 + jj;
-              if (j <= t && (j > t - a.window || j - bos < a.first)) mask |= 1u << jj;
+              if (j <= t && j > t - a.window) mask |= 1u << jj;
             }
           }
         }
@@ -394,16 +394,120 @@ __global__ void __launch_bounds__(kThreads) bwd_dkdv_kernel(const BwdParams a, i
       }
       for (int e = tid; e < n * dk; e += kThreads) {
         const int jj = e / dk, d = e - jj * dk;
-        st<T>(a.dkey, (int64_t)(s0 + jj) * dk + d, dks[e], a.like_input);
+        static_cast<float*>(a.dkey)[(int64_t)(s0 + jj) * dk + d] = dks[e];
       }
       for (int e = tid; e < n * dv; e += kThreads) {
         const int jj = e / dv, d = e - jj * dv;
-        st<T>(a.dval, (int64_t)(s0 + jj) * dv + d, dvs[e], a.like_input);
+        static_cast<float*>(a.dval)[(int64_t)(s0 + jj) * dv + d] = dvs[e];
       }
       __syncthreads();
       s0 = s1;
     }
   }
+}
+
+// dk and dv of the window with visible first tokens, any shape: a block per
+// key.  A warp takes every kWarps-th (query, head) that sees the key, lanes over
+// the columns: two dot products, then its share of the sums in registers.  A
+// first token of the tile kernel above would meet every query of its document
+// one after the other in one block (1.5 ms at 400 tokens, 4 heads, Dk 64; here
+// 0.03 ms).  Only rows that see the key are read; sums go in a fixed order.
+template <typename T, int NK, int NV, int kWarps>
+__global__ void __launch_bounds__(kWarps * 32) bwd_key_kernel(const BwdParams a) {
+  constexpr int U = NK <= 2 ? 4 : 1;  // (query, head)s of a warp at a time
+  __shared__ float red[kWarps][32];
+  const Problem& P = a.p;
+  const int H = P.num_heads, dk = P.dk, dv = P.dv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int j = blockIdx.x; j < P.total_tokens; j += gridDim.x) {
+    if (a.only && __ldg(a.only + j) == 0) continue;
+    int bos, eos;
+    if (!find_doc(P.cu_seqlens, P.num_docs, P.total_tokens, P.max_seqlen, j, bos, eos, P.status))
+      continue;
+    const int tend = j - bos < a.first || eos - j <= a.window ? eos : j + a.window;
+    const int64_t n = (int64_t)(tend - j) * H;
+    float k[NK], v[NV], ak[NK], av[NV];
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      ak[i] = 0.f;
+      k[i] = lane + 32 * i < dk ? ld<T>(P.k, (int64_t)j * P.k_row_stride + lane + 32 * i) : 0.f;
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      av[i] = 0.f;
+      v[i] = lane + 32 * i < dv ? ld<T>(P.v, (int64_t)j * P.v_row_stride + lane + 32 * i) : 0.f;
+    }
+    for (int64_t e0 = warp; e0 < n; e0 += U * kWarps) {
+      float q[U][NK], o[U][NV], s[U], d[U], lse[U], del[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int64_t e = e0 + u * kWarps;
+        const bool in = e < n;
+        const int t = j + (in ? (int)(e / H) : 0), h = in ? (int)(e % H) : 0;
+        const int64_t th = (int64_t)t * H + h;
+        const int64_t qb = (int64_t)t * P.q_row_stride + (int64_t)h * P.q_head_stride;
+        s[u] = d[u] = 0.f;
+        lse[u] = in ? __ldg(a.lse + th) : INFINITY;  // exp(s - inf) = 0
+        del[u] = in ? __ldg(a.delta + th) : 0.f;
+#pragma unroll
+        for (int i = 0; i < NK; ++i) {
+          q[u][i] = in && lane + 32 * i < dk ? ld<T>(P.q, qb + lane + 32 * i) : 0.f;
+          s[u] = fmaf(q[u][i], k[i], s[u]);
+        }
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          o[u][i] = in && lane + 32 * i < dv ? ld<T>(a.dout, th * dv + lane + 32 * i) : 0.f;
+          d[u] = fmaf(o[u][i], v[i], d[u]);
+        }
+      }
+#pragma unroll
+      for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          s[u] += __shfl_xor_sync(0xffffffffu, s[u], off);
+          d[u] += __shfl_xor_sync(0xffffffffu, d[u], off);
+        }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        if (e0 + u * kWarps >= n) continue;
+        const float p = expf(s[u] * P.scale - lse[u]), ds = P.scale * p * (d[u] - del[u]);
+#pragma unroll
+        for (int i = 0; i < NK; ++i) ak[i] = fmaf(ds, q[u][i], ak[i]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i) av[i] = fmaf(p, o[u][i], av[i]);
+      }
+    }
+    // the warps' sums, 32 columns at a time
+    auto join = [&](float x, int col, int width, void* out) {
+      red[warp][lane] = x;
+      __syncthreads();
+      if (warp == 0 && col + lane < width) {
+        float sum = 0.f;
+        for (int w = 0; w < kWarps; ++w) sum += red[w][lane];
+        st<T>(out, (int64_t)j * width + col + lane, sum, a.like_input);
+      }
+      __syncthreads();
+    };
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+      if (32 * i < dk) join(ak[i], 32 * i, dk, a.dkey);
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+      if (32 * i < dv) join(av[i], 32 * i, dv, a.dval);
+  }
+}
+
+template <typename T>
+cudaError_t launch_keys(const BwdParams& a, cudaStream_t s) {
+  const int most = a.p.dk > a.p.dv ? a.p.dk : a.p.dv;
+  const int grid = a.only && a.p.total_tokens > 592 ? 592 : a.p.total_tokens;
+  if (most <= 64)
+    bwd_key_kernel<T, 2, 2, 16><<<grid, 512, 0, s>>>(a);
+  else if (most <= 256)
+    bwd_key_kernel<T, 8, 8, 16><<<grid, 512, 0, s>>>(a);
+  else
+    bwd_key_kernel<T, 32, 32, 8><<<grid, 256, 0, s>>>(a);
+  return cudaGetLastError();
 }
 
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -447,6 +551,7 @@ cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
     e = launch_dq<T, kSparse>(a, s);
     if (e != cudaSuccess) return e;
   }
+  if (cuda_core_passes && a.with_first) return launch_keys<T>(a, s);
   // dk, dv: key tiles of at most kKeyTile keys (unless the caller runs the
   // tensor-core key-major pass instead)
   if (cuda_core_passes) {
@@ -490,6 +595,7 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
   a.dsink = b.dsink;
   a.first = b.first;
   a.like_input = b.grad_like_input;
+  a.with_first = b.with_first;
   a.delta = static_cast<float*>(b.workspace);
   a.dsink_part = a.delta + (size_t)b.p.total_tokens * b.p.num_heads;
   if (b.p.dtype == HS_BF16) {
@@ -501,29 +607,35 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
                            : launch_typed<__nv_bfloat16, false>(a, !mma, s);
     if (e != cudaSuccess || !mma) return e;
     // With visible first tokens nothing outside the key sets may show: a dq
-    // that a key outside spoiled (0 * NaN in a whole-tile product) is flagged
-    // and computed again.  The sink terms' place is free for the flags.
+    // that a key outside spoiled, and a dk or dv that a query outside spoiled
+    // (0 * NaN in a whole-tile product), is flagged and computed again.  The
+    // sink terms' place (64 heads) is free for both flags.
+    const size_t nt = (size_t)b.p.total_tokens;
     int* const flags = b.with_first ? reinterpret_cast<int*>(a.dsink_part) : nullptr;
+    int* const kflags = flags ? flags + nt : nullptr;
     if (flags) {
-      e = cudaMemsetAsync(flags, 0, sizeof(int) * (size_t)b.p.total_tokens, s);
+      e = cudaMemsetAsync(flags, 0, 2 * sizeof(int) * nt, s);
       if (e != cudaSuccess) return e;
     }
     bool taken = false;  // the window's own passes, where their workspace was given
     if (flags) {
-      e = launch_tc_first_bwd(b, a.delta, flags, b.dkdv_ws, b.dkdv_bytes, 0, &taken, s);
+      e = launch_tc_first_bwd(b, a.delta, flags, kflags, b.dkdv_ws, b.dkdv_bytes, 0, &taken, s);
       if (e != cudaSuccess) return e;
     }
     if (!taken) {
       e = launch_tc_bwd_dq(b, sparse, a.delta, flags, 0, s);
       if (e != cudaSuccess) return e;
     }
-    if (flags) {
-      a.only = flags;
-      e = launch_dq<__nv_bfloat16, false>(a, s);
+    if (!taken) {
+      e = launch_tc_bwd_dkdv(b, sparse, a.delta, kflags, 0, s);
       if (e != cudaSuccess) return e;
     }
-    if (taken) return cudaSuccess;
-    return launch_tc_bwd_dkdv(b, sparse, a.delta, 0, s);
+    if (!flags) return cudaSuccess;
+    a.only = flags;
+    e = launch_dq<__nv_bfloat16, false>(a, s);
+    if (e != cudaSuccess) return e;
+    a.only = kflags;
+    return launch_keys<__nv_bfloat16>(a, s);
   }
   if (path) *path = HS_PATH_SIMT;
   return sparse ? launch_typed<float, true>(a, true, s) : launch_typed<float, false>(a, true, s);

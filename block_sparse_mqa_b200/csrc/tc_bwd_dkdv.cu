@@ -73,6 +73,7 @@ struct DkdvParams {
   void* dkey;          // fp32, or bf16 (like_input)
   void* dval;
   bool like_input;
+  int* spoiled;        // set to 1 per key whose dk or dv is not finite, or null
   int* status;
   long long wait_ns;
   // work items: (32-key tile, query range) pairs, range-major
@@ -568,6 +569,7 @@ __global__ void __launch_bounds__(256) dkdv_reduce_kernel(const DkdvParams p) {
     void* const dst = col < p.dk ? p.dkey : p.dval;
     const int64_t at = col < p.dk ? (int64_t)j * p.dk + col : (int64_t)j * p.dv + (col - p.dk);
     if (col < p.dk) sum *= p.scale;
+    if (p.spoiled && !isfinite(sum)) p.spoiled[j] = 1;
     if (p.like_input)
       static_cast<__nv_bfloat16*>(dst)[at] = __float2bfloat16_rn(sum);
     else
@@ -605,7 +607,7 @@ bool tc_bwd_dkdv_supported(const Problem& p) {
          p.q_head_stride % 8 == 0 && p.k_row_stride % 8 == 0 && p.v_row_stride % 8 == 0;
 }
 
-cudaError_t launch_tc_bwd_dkdv(const BwdArgs& b, bool sparse, const float* delta,
+cudaError_t launch_tc_bwd_dkdv(const BwdArgs& b, bool sparse, const float* delta, int* spoiled,
                                long long wait_limit, cudaStream_t s) {
   const Problem& p = b.p;
   if (reinterpret_cast<uintptr_t>(b.dout) & 15) return cudaErrorInvalidValue;
@@ -655,6 +657,7 @@ cudaError_t launch_tc_bwd_dkdv(const BwdArgs& b, bool sparse, const float* delta
   a.dkey = b.dkey;
   a.dval = b.dval;
   a.like_input = b.grad_like_input;
+  a.spoiled = spoiled;
   a.status = p.status;
   a.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
   range_split(p.total_tokens, a.rlen, a.nrange);

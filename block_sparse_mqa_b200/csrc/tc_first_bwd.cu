@@ -779,7 +779,8 @@ key_pass(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
 // dk and dv of one key: its partial sums in order.  The ones that no job wrote
 // (no token in them) are left out by the jobs' own rule.
 __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, float scale,
-                                              __nv_bfloat16* dkey, __nv_bfloat16* dval) {
+                                              __nv_bfloat16* dkey, __nv_bfloat16* dval,
+                                              int* spoiled) {
   const int W = p.dk + p.dv;
   for (int j = blockIdx.x; j < p.d.T; j += gridDim.x) {
     const int tile = j / kKeys, key0 = tile * kKeys;
@@ -815,6 +816,7 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
         add(p.fpart + ((int64_t)(c + doc) * p.band.fp + f) * W + col);
       const bool is_k = col < p.dk;
       const float m = is_k ? scale : 1.f;
+      if (!(isfinite(s.x) && isfinite(s.y) && isfinite(s.z) && isfinite(s.w))) spoiled[j] = 1;
       __nv_bfloat162* const o = reinterpret_cast<__nv_bfloat162*>(
           is_k ? dkey + (int64_t)j * p.dk + col : dval + (int64_t)j * p.dv + (col - p.dk));
       o[0] = __floats2bfloat162_rn(m * s.x, m * s.y);
@@ -863,8 +865,8 @@ size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, in
   return n <= kMostBytes ? n : 0;
 }
 
-cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled, void* ws,
-                                size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s) {
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled,
+                                int* spoiled_keys, void* ws, size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s) {
   *taken = false;
   const Problem& p = b.p;
   Band band;
@@ -948,7 +950,7 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   pb::reduce<<<std::min(T, 148 * 8), 256, 0, s>>>(k, p.scale, static_cast<__nv_bfloat16*>(b.dkey),
-                                                 static_cast<__nv_bfloat16*>(b.dval));
+                                                 static_cast<__nv_bfloat16*>(b.dval), spoiled_keys);
   return cudaGetLastError();
 }
 

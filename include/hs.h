@@ -433,8 +433,8 @@ hs_status hs_swa_first_mqa_fwd(const void* q, int64_t q_row_stride, int64_t q_he
  * (token, head, attended key) as bf16 (4096 tokens, window 512: 0.7 GB), up to
  * 4 GB; beyond that slower passes run that need less.
  * A query whose own q, dout, out or lse row holds NaN or an infinity spoils
- * the gradients of the keys it attends, and may spoil those of the up to 31
- * neighbours of such a key in the same document.
+ * the gradients of the keys it attends, and a key that does the dq of the
+ * queries that attend it; no others.
  */
 hs_status hs_swa_first_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_head_stride,
                                const void* k, int64_t k_row_stride,

@@ -225,3 +225,66 @@ def test_no_tokens():
     assert out.shape == (0, 64, 512) and lse.shape == (0, 64)
     g = hs.hs_swa_first_mqa_bwd(q, k, v, cu, 1, 4, 1, out, lse, out, sink)
     assert g[0].shape == (0, 64, 576) and not g[3].any()
+
+
+@pytest.mark.parametrize("W,F", [(30, 4), (100, 0), (20, 300)])
+def test_a_spoiled_query_spoils_only_its_own_keys(W, F):
+    """NaN in a query's q and infinity in another's dout: keys that neither sees
+    keep their gradients, in every document.  (20, 300): more first tokens than
+    the band takes."""
+    docs = [400, 150, 333]
+    inp, dout = _inputs(docs, 64, 192, 128, BF16, 12)
+    cu = inp.cu_seqlens.tolist()
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 400, W, F, inp.sink)
+    bad = [211, 430]
+    inp.q[bad[0], 3, 7] = float("nan")
+    dout[bad[1], 60, 100] = float("inf")
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 400, W, F, out, lse, dout, inp.sink)
+    hs.poll_status()
+    mask = A.mask_of(cu, W, F, DEV)
+    rows = torch.ones(sum(docs), dtype=torch.bool, device=DEV)
+    rows[bad] = False
+    keys = ~mask[bad].any(0)
+    ref = A.backward(inp.q[rows], inp.k, inp.v, out[rows], lse[rows], dout[rows], mask[rows], None,
+                     192 ** -0.5, BF16)
+    assert 300 < int(keys.sum()) < sum(docs)
+    A.check(g[0][rows], *ref["dq"], "dq")
+    for i, name in ((1, "dk"), (2, "dv")):
+        A.check(g[i][keys], *(x[keys] for x in ref[name]), name)
+    assert bool(g[1][bad[0]].isnan().any()) and not bool(g[2][bad[1]].isfinite().all())
+
+
+@pytest.mark.parametrize("docs,W,F", [([700, 30, 900], 64, 250), ([1200, 64, 65, 300], 40, 33), ([2100, 90], 300, 5),
+                                      ([600], 50, 257), ([128] * 9 + [1], 127, 3), ([513, 511], 512, 1)])
+def test_first_tokens_over_chunks_and_documents(docs, W, F):
+    """Documents that begin and end inside token chunks and key tiles, first tokens
+    up to and past what the band takes."""
+    _run(docs, 64, 128, 64, BF16, W, F, seed=13)
+
+
+def test_other_passes_without_the_band():
+    """A workspace that has no room for the band: the window passes' own."""
+    docs, W, F = [300, 290], 100, 6
+    inp, dout = _inputs(docs, 64, 192, 128, BF16, 14)
+    args = (inp.cu_seqlens, 300, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    want = hs.workspace_size(hs.HS_OP_SWA_FIRST_MQA_BWD, 590, 2, 300, 64, 192, 128, BF16, W + F)
+    with pytest.raises(hs.HSError) as e:
+        hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink,
+                                workspace=torch.empty(want - 1, dtype=torch.uint8, device=DEV))
+    assert e.value.status == hs.HS_ERR_WORKSPACE
+    big = torch.full((want + 5000,), 0xFF, dtype=torch.uint8, device=DEV)  # NaN wherever it is read first
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink, workspace=big)
+    hs.poll_status()
+    assert bool((big[want:] == 0xFF).all())
+    _check_bwd(inp, W, F, inp.sink, out, lse, dout, g, BF16)
+
+
+def test_without_tensor_cores():
+    """The CUDA-core kernels at the shape that normally does not reach them."""
+    hs.set_force_simt(True)
+    try:
+        _run([90, 41, 1], 64, 192, 128, BF16, 20, 3, seed=15, path=(hs.HS_PATH_SIMT, hs.HS_PATH_SIMT))
+    finally:
+        hs.set_force_simt(False)
+    _run([90, 41, 1], 64, 192, 128, BF16, 20, 3, seed=15, path=(hs.HS_PATH_TCGEN05, hs.HS_PATH_MMA))
