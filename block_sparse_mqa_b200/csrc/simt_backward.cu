@@ -103,6 +103,34 @@ __global__ void __launch_bounds__(kThreads) bwd_delta_kernel(const BwdParams a) 
   }
 }
 
+// The same for aligned bf16 rows: every load of a row under way at once (114 ->
+// 90 us at 4096 tokens, 64 heads, Dv 512, where 0.54 GB have to be read).
+__global__ void __launch_bounds__(kThreads) bwd_delta16_kernel(const BwdParams a) {
+  const int64_t th = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
+  const int lane = threadIdx.x & 31, dv = a.p.dv, units = dv / 8;
+  if (th >= (int64_t)a.p.total_tokens * a.p.num_heads) return;
+  const uint4* const o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + th * dv);
+  const uint4* const d = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + th * dv);
+  float acc = 0.f;
+#pragma unroll 2
+  for (int e = lane; e < units; e += 32) {
+    const uint4 x = __ldcs(o + e), y = __ldg(d + e);
+    const __nv_bfloat162* const xp = reinterpret_cast<const __nv_bfloat162*>(&x);
+    const __nv_bfloat162* const yp = reinterpret_cast<const __nv_bfloat162*>(&y);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float2 u = __bfloat1622float2(xp[k]), v = __bfloat1622float2(yp[k]);
+      acc = fmaf(u.x, v.x, fmaf(u.y, v.y, acc));
+    }
+  }
+  acc = warp_sum(acc);
+  if (lane == 0) {
+    const int h = (int)(th % a.p.num_heads);
+    a.delta[th] = acc;
+    a.dsink_part[th] = a.sink ? -expf(__ldg(a.sink + h) - __ldg(a.lse + th)) * acc : 0.f;
+  }
+}
+
 // ---------------------------------------------------------------- dsink
 __global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a) {
   __shared__ float red[kThreads];
@@ -130,6 +158,15 @@ __host__ __device__ inline size_t dq_smem_floats(int G, int KT, int dk, int dv) 
          (size_t)G * dk + 2 * (size_t)G * KT + 2 * (size_t)G;
 }
 
+// Is any of this block's tokens (blockIdx.x, + gridDim.x, ...) listed in a.only?
+__device__ __forceinline__ bool any_listed(const BwdParams& a) {
+  int any = 0;
+  for (int64_t t = blockIdx.x + (int64_t)threadIdx.x * gridDim.x; t < a.p.total_tokens;
+       t += (int64_t)blockDim.x * gridDim.x)
+    any |= __ldg(a.only + t);
+  return __syncthreads_or(any);
+}
+
 template <typename T, bool kSparse>
 __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
   extern __shared__ float sm[];
@@ -148,6 +185,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
   float* del_s = lse_s + G;
   int* blist = reinterpret_cast<int*>(del_s + G);
   const float scale = P.scale;
+  if (a.only && !any_listed(a)) return;
   for (int t = blockIdx.x; t < P.total_tokens; t += gridDim.x) {
     if (a.only && __ldg(a.only + t) == 0) continue;
     int bos, eos;
@@ -419,6 +457,7 @@ __global__ void __launch_bounds__(kWarps * 32) bwd_key_kernel(const BwdParams a)
   const Problem& P = a.p;
   const int H = P.num_heads, dk = P.dk, dv = P.dv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (a.only && !any_listed(a)) return;
   for (int j = blockIdx.x; j < P.total_tokens; j += gridDim.x) {
     if (a.only && __ldg(a.only + j) == 0) continue;
     int bos, eos;
@@ -500,7 +539,7 @@ __global__ void __launch_bounds__(kWarps * 32) bwd_key_kernel(const BwdParams a)
 template <typename T>
 cudaError_t launch_keys(const BwdParams& a, cudaStream_t s) {
   const int most = a.p.dk > a.p.dv ? a.p.dk : a.p.dv;
-  const int grid = a.only && a.p.total_tokens > 592 ? 592 : a.p.total_tokens;
+  const int grid = a.only && a.p.total_tokens > 148 ? 148 : a.p.total_tokens;
   if (most <= 64)
     bwd_key_kernel<T, 2, 2, 16><<<grid, 512, 0, s>>>(a);
   else if (most <= 256)
@@ -528,7 +567,7 @@ cudaError_t launch_dq(BwdParams a, cudaStream_t s) {
   cudaError_t e =
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
-  const int grid = a.only && P.total_tokens > 592 ? 592 : P.total_tokens;
+  const int grid = a.only && P.total_tokens > 148 ? 148 : P.total_tokens;
   kern<<<grid, kThreads, bytes, s>>>(a);
   return cudaGetLastError();
 }
@@ -538,7 +577,13 @@ cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
   const Problem& P = a.p;
   const int NT = P.total_tokens, H = P.num_heads;
   const int pairs = NT * H;
-  bwd_delta_kernel<T><<<(pairs + kThreads / 32 - 1) / (kThreads / 32), kThreads, 0, s>>>(a);
+  const unsigned blocks = (unsigned)((pairs + kThreads / 32 - 1) / (kThreads / 32));
+  const bool wide = a.with_first && P.dtype == HS_BF16 && P.dv % 8 == 0 &&
+                    ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.dout)) & 15) == 0;
+  if (wide)
+    bwd_delta16_kernel<<<blocks, kThreads, 0, s>>>(a);
+  else
+    bwd_delta_kernel<T><<<blocks, kThreads, 0, s>>>(a);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.dsink && a.sink) {

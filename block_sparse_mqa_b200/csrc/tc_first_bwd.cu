@@ -545,7 +545,7 @@ struct Shared {
   uint64_t full[kStages], empty[kStages], done, freed, drain;
   uint32_t tmem_base;
 };
-constexpr size_t kSmem = 1024 + (size_t)kStages * kStageBytes + sizeof(Shared);
+constexpr size_t kSmem = (size_t)kStages * kStageBytes + sizeof(Shared);
 
 // One accumulation: tokens [t0, t1) against n keys, columns [col0, col0 + cols)
 // of q (dk) or dout (dv), into a partial sum.
@@ -633,9 +633,12 @@ key_pass(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
          const __grid_constant__ CUtensorMap pwmap, const __grid_constant__ CUtensorMap pfmap,
          const __grid_constant__ CUtensorMap swmap, const __grid_constant__ CUtensorMap sfmap,
          const __grid_constant__ Params p) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t* const ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                                   ~static_cast<uintptr_t>(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  if (smem_u32(smem_raw) & 1023) {
+    record_status(p.status, HS_ERR_CUDA);
+    return;  // every thread of both CTAs alike
+  }
+  uint8_t* const ring = smem_raw;
   Shared* sh = reinterpret_cast<Shared*>(ring + kStages * kStageBytes);
   const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
   const int rank = (int)cluster_rank();
