@@ -188,6 +188,7 @@ def _qk_strides(q, k):
 
 def set_force_simt(on: bool):
     lib().hs_set_force_simt(1 if on else 0)
+    _sizes.cache_clear()
 
 
 def selftest_wait(limit_ns: int, device=None):
@@ -217,6 +218,12 @@ def workspace_size(op, total_tokens, num_docs, max_seqlen, num_heads, dk, dv, dt
     code = HS_BF16 if dtype == torch.bfloat16 else HS_F32
     return int(lib().hs_workspace_size(op, total_tokens, num_docs, max_seqlen, num_heads, dk, dv,
                                        code, block_size))
+
+
+@functools.lru_cache(maxsize=1024)
+def _sizes(*args) -> int:
+    """workspace_size of the calls that serve single tokens: sizes alone decide it."""
+    return workspace_size(*args)
 
 
 def nbmax(max_seqlen: int, block_size: int) -> int:
@@ -546,6 +553,14 @@ def _out(name, t, shape, dtype):
         raise ValueError("%s must be contiguous %s %s" % (name, dtype, list(shape)))
 
 
+def _new_or(t, name, shape, dtype, like):
+    """t, checked, or a new tensor on `like`'s device."""
+    if t is None:
+        return torch.empty(shape, device=like.device, dtype=dtype)
+    _out(name, t, shape, dtype)
+    return t
+
+
 def _sink_ok(sink, H):
     if sink is not None:
         _out("sink", sink, (H,), torch.float32)
@@ -571,9 +586,8 @@ def hs_swa_first_mqa_fwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
     Returns (out [T,H,Dv] in q's dtype, lse [T,H] f32)."""
     index, T, H, Dk, Dv = _swa_first_check(q, k, v, cu_seqlens, sink, out, lse)
     qrs, qhs = _q_strides(q)
-    o, l = _attn_out(q, v, out, lse)
-    _out("out", o, (T, H, Dv), q.dtype)
-    _out("lse", l, (T, H), torch.float32)
+    o = _new_or(out, "out", (T, H, Dv), q.dtype, q)
+    l = _new_or(lse, "lse", (T, H), torch.float32, q)
     if T == 0:
         return o, l
     _call(lib().hs_swa_first_mqa_fwd, index, _addr(q), qrs, qhs, _addr(k), _row_stride(k),
@@ -608,8 +622,8 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
         return grads
     if workspace is None:
         span = min(int(window), int(max_seqlen)) + min(int(num_first), int(max_seqlen))
-        workspace = torch.empty(workspace_size(HS_OP_SWA_FIRST_MQA_BWD, T, nd, max_seqlen, H, Dk,
-                                               Dv, q.dtype, span),
+        workspace = torch.empty(_sizes(HS_OP_SWA_FIRST_MQA_BWD, T, nd, int(max_seqlen), H, Dk, Dv,
+                                       q.dtype, span),
                                 device=q.device, dtype=torch.uint8)
     _call(lib().hs_swa_first_mqa_bwd, index, _addr(q), qrs, qhs, _addr(k), _row_stride(k),
           _addr(v), _row_stride(v), _addr(cu_seqlens), nd, T, int(max_seqlen), H, Dk, Dv,
@@ -647,11 +661,11 @@ def _plane(name, cache, width, page_size, like=None):
 def _table_args(block_table, seq_lens, num_pages, page_size):
     _int32("block_table", block_table, 2)
     _int32("seq_lens", seq_lens)
-    if block_table.shape[0] != seq_lens.numel():
+    rows, width = block_table.shape
+    if rows != seq_lens.shape[0]:
         raise ValueError("block_table must have one row per sequence")
     # a single row's stride may be anything; the library wants at least the width
-    stride = max(block_table.stride(0), block_table.shape[1])
-    return _addr(block_table), stride, block_table.shape[1], num_pages, int(page_size)
+    return block_table.data_ptr(), max(block_table.stride(0), width), width, num_pages, int(page_size)
 
 
 def hs_kv4_append(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens, page_size: int):
@@ -720,15 +734,13 @@ def hs_kv4_mqa_decode(q, k_cache, v_cache, block_table, seq_lens, max_seqlen: in
         _plane("v_cache", v_cache, dv, page_size, k_cache)
     table = _table_args(block_table, seq_lens, k_cache.shape[0], page_size)
     _sink_ok(sink, H)
-    o = out if out is not None else torch.empty((S, H, dv), device=q.device, dtype=q.dtype)
-    l = lse if lse is not None else torch.empty((S, H), device=q.device, dtype=torch.float32)
-    _out("out", o, (S, H, dv), q.dtype)
-    _out("lse", l, (S, H), torch.float32)
+    o = _new_or(out, "out", (S, H, dv), q.dtype, q)
+    l = _new_or(lse, "lse", (S, H), torch.float32, q)
     if S == 0:
         return o, l
     if workspace is None:
-        workspace = torch.empty(workspace_size(HS_OP_KV4_MQA_DECODE, S, S, max_seqlen, H, Dk, dv,
-                                               q.dtype, page_size),
+        workspace = torch.empty(_sizes(HS_OP_KV4_MQA_DECODE, S, S, int(max_seqlen), H, Dk, int(dv),
+                                       q.dtype, int(page_size)),
                                 device=q.device, dtype=torch.uint8)
     _call(lib().hs_kv4_mqa_decode, index, _addr(q), qrs, qhs, _addr(k_cache), _addr(v_cache),
           *table, _addr(seq_lens), S, int(max_seqlen), H, Dk, int(dv), _dtype_code(q),
