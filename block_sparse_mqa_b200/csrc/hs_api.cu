@@ -595,7 +595,10 @@ static hs_status backward_common(hs::BwdArgs& a, bool sparse, const void* q, int
   a.dsink = dsink;
   if (total_tokens == 0) return HS_OK;
   int span = 0;  // of keys, none of them past a document
-  if (a.with_first) span = std::min(a.window, max_seqlen) + std::min(a.first, max_seqlen);
+  if (a.with_first) {
+    const int most = std::min(max_seqlen, total_tokens);
+    span = std::min(a.window, most) + std::min(a.first, most);
+  }
   const size_t need = bwd_workspace(total_tokens, num_heads, dk, dv, dtype, num_docs, max_seqlen, span);
   if (!workspace || workspace_bytes < need)
     return fail(HS_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,

@@ -859,8 +859,9 @@ constexpr size_t kMostBytes = (size_t)4 << 30;  // of workspace; beyond it the o
 
 size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, int span, int dk,
                               int dv) {
+  max_seqlen = std::min(max_seqlen, total_tokens);  // a loose bound costs nothing
   if (span < 1) span = 1;
-  if (span > 2 * max_seqlen) span = 2 * max_seqlen;
+  if (span / 2 >= max_seqlen) span = 2 * max_seqlen;
   // the most any split of the span into window and first tokens needs
   const int fp = std::min((span + 15) & ~15, pb::kKeys);
   const Sizes z = sizes_of(total_tokens, num_docs, span, std::min(span, max_seqlen), fp, dk, dv);
@@ -873,9 +874,10 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   *taken = false;
   const Problem& p = b.p;
   Band band;
-  band.window = std::min(b.window, p.max_seqlen);
+  const int longest = std::min(p.max_seqlen, p.total_tokens);
+  band.window = std::min(b.window, longest);
   // a window that holds every document leaves no first token outside
-  band.first = band.window >= p.max_seqlen ? 0 : std::min(b.first, p.max_seqlen);
+  band.first = band.window >= longest ? 0 : std::min(b.first, longest);
   band.wp = (band.window - 1 + 7) & ~7;
   band.bw = (band.wp + 8 + 15) & ~15;
   band.fp = (band.first + 15) & ~15;

@@ -621,7 +621,8 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
             grads[3].zero_()
         return grads
     if workspace is None:
-        span = min(int(window), int(max_seqlen)) + min(int(num_first), int(max_seqlen))
+        most = min(int(max_seqlen), T)
+        span = min(int(window), most) + min(int(num_first), most)
         workspace = torch.empty(_sizes(HS_OP_SWA_FIRST_MQA_BWD, T, nd, int(max_seqlen), H, Dk, Dv,
                                        q.dtype, span),
                                 device=q.device, dtype=torch.uint8)

@@ -427,9 +427,9 @@ hs_status hs_swa_first_mqa_fwd(const void* q, int64_t q_row_stride, int64_t q_he
  * dq [T, H, Dk], dkey [T, Dk] and dval [T, Dv] are of `dtype`, the type of
  * the tensors they belong to (step 4's backward returns fp32): sums run in
  * fp32 and are rounded once.  dsink [H] is fp32.  Results are deterministic.
- * Workspace: hs_workspace_size(HS_OP_SWA_FIRST_MQA_BWD, ...) with min(window,
- * max_seqlen) + min(num_first, max_seqlen) in the place of block_size, and the
- * rules of hs_sparse_mqa_bwd.  On tensor cores it holds P and dS of every
+ * Workspace: hs_workspace_size(HS_OP_SWA_FIRST_MQA_BWD, ...) with min(window, L)
+ * + min(num_first, L), L = min(max_seqlen, total_tokens), in the place of
+ * block_size, and the rules of hs_sparse_mqa_bwd.  On tensor cores it holds P and dS of every
  * (token, head, attended key) as bf16 (4096 tokens, window 512: 0.7 GB), up to
  * 4 GB; beyond that slower passes run that need less.
  * A query whose own q, dout, out or lse row holds NaN or an infinity spoils

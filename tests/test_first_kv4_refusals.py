@@ -88,6 +88,14 @@ def test_nothing_to_do_is_no_error():
     assert _call("hs_kv4_mqa_decode", DECODE, dict(S=0, maxlen=0, ws=None)) == hs.HS_OK
 
 
+def test_backward_workspace_of_a_loose_bound():
+    """A max_seqlen above the tokens there are asks for no more than the tokens do."""
+    size = lambda maxlen, span: hs.workspace_size(hs.HS_OP_SWA_FIRST_MQA_BWD, 1000, 2, maxlen, 64, 576, 512,
+                                                  torch.bfloat16, span)
+    assert size(10 ** 6, 2000) == size(1000, 2000) > 2 ** 28
+    assert size(10 ** 6, 40) == size(1000, 40) < size(10 ** 6, 2000)
+
+
 def test_page_bytes():
     assert hs.kv4_page_bytes(32, 16) == 16 * 20
     assert hs.kv4_page_bytes(512, 64) == 64 * (256 + 16)  # 4.25 bits an element

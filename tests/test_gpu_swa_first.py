@@ -280,6 +280,18 @@ def test_other_passes_without_the_band():
     _check_bwd(inp, W, F, inp.sink, out, lse, dout, g, BF16)
 
 
+def test_a_loose_bound_of_the_lengths():
+    """max_seqlen, window and num_first far above the tokens there are."""
+    docs, far = [700, 1], 200000
+    inp, dout = _inputs(docs, 64, 64, 64, BF16, 16)
+    args = (inp.cu_seqlens, far, far, far)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink)
+    hs.poll_status()
+    _check_fwd(inp, far, far, inp.sink, out, lse, BF16)
+    _check_bwd(inp, far, far, inp.sink, out, lse, dout, g, BF16)
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
