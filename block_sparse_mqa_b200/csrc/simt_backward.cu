@@ -645,8 +645,11 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
   a.dsink_part = a.delta + (size_t)b.p.total_tokens * b.p.num_heads;
   if (b.p.dtype == HS_BF16) {
     // tensor cores: dq and dk / dv on tcgen05 (else every pass on CUDA cores)
+    auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
     const bool mma = allow_mma && tc_bwd_dq_supported(b.p) && tc_bwd_dkdv_supported(b.p) &&
-                     (reinterpret_cast<uintptr_t>(b.dout) & 15) == 0 && b.dkdv_ws != nullptr;
+                     al16(b.dout) && b.dkdv_ws != nullptr &&
+                     // bf16 gradients are stored 16 and 4 bytes at a time
+                     (!b.grad_like_input || (al16(b.dq) && al16(b.dkey) && al16(b.dval)));
     if (path) *path = mma ? HS_PATH_MMA : HS_PATH_SIMT;
     cudaError_t e = sparse ? launch_typed<__nv_bfloat16, true>(a, !mma, s)
                            : launch_typed<__nv_bfloat16, false>(a, !mma, s);

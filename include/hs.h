@@ -431,7 +431,8 @@ hs_status hs_swa_first_mqa_fwd(const void* q, int64_t q_row_stride, int64_t q_he
  * + min(num_first, L), L = min(max_seqlen, total_tokens), in the place of
  * block_size, and the rules of hs_sparse_mqa_bwd.  On tensor cores it holds P and dS of every
  * (token, head, attended key) as bf16 (4096 tokens, window 512: 0.7 GB), up to
- * 4 GB; beyond that slower passes run that need less.
+ * 4 GB; beyond that slower passes run that need less.  Gradients that are not
+ * 16-byte aligned take the CUDA-core passes.
  * A query whose own q, dout, out or lse row holds NaN or an infinity spoils
  * the gradients of the keys it attends, and a key that does the dq of the
  * queries that attend it; no others.

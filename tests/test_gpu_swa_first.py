@@ -292,6 +292,27 @@ def test_a_loose_bound_of_the_lengths():
     _check_bwd(inp, far, far, inp.sink, out, lse, dout, g, BF16)
 
 
+@pytest.mark.parametrize("which", [0, 1, 2])
+def test_gradients_at_any_element(which):
+    """dq, dk or dv one element past a 16-byte boundary; nothing beside them is written."""
+    docs, W, F = [130, 41], 30, 4
+    inp, dout = _inputs(docs, 64, 64, 128, BF16, 17)
+    args = (inp.cu_seqlens, 130, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    grads, holds = [], []
+    for i, x in enumerate((inp.q, inp.k, dout[:, 0])):
+        off = int(i == which)
+        holds.append(torch.full((x.numel() + 16,), 7.0, device=DEV, dtype=BF16))
+        grads.append(holds[i][off:off + x.numel()].view(x.shape))
+    grads.append(torch.empty(64, device=DEV))
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink, grads=grads)
+    hs.poll_status()
+    _check_bwd(inp, W, F, inp.sink, out, lse, dout, g, BF16)
+    for i, h in enumerate(holds):
+        off = int(i == which)
+        assert bool((h[:off] == 7).all()) and bool((h[off + grads[i].numel():] == 7).all())
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
