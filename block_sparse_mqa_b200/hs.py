@@ -665,8 +665,9 @@ def _table_args(block_table, seq_lens, num_pages, page_size):
     rows, width = block_table.shape
     if rows != seq_lens.shape[0]:
         raise ValueError("block_table must have one row per sequence")
-    # a single row's stride may be anything; the library wants at least the width
-    return block_table.data_ptr(), max(block_table.stride(0), width), width, num_pages, int(page_size)
+    # a single row's stride may be anything; the library refuses one below the width
+    stride = block_table.stride(0) if rows > 1 else max(block_table.stride(0), width)
+    return block_table.data_ptr(), stride, width, num_pages, int(page_size)
 
 
 def hs_kv4_append(k, v, k_cache, v_cache, block_table, cu_seqlens, seq_lens, page_size: int):

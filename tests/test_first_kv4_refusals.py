@@ -96,6 +96,17 @@ def test_backward_workspace_of_a_loose_bound():
     assert size(10 ** 6, 40) == size(1000, 40) < size(10 ** 6, 2000)
 
 
+def test_table_strides():
+    """A table of one row has the stride it likes; rows that overlap are not taken for rows side by side."""
+    lens = torch.zeros(3, dtype=torch.int32)
+    stride = lambda table: hs._table_args(table, lens[:table.shape[0]], 5, 16)[1]
+    one = torch.zeros((1, 4), dtype=torch.int32)
+    assert stride(one) == 4 and stride(one[:, 1:]) >= 3
+    assert stride(torch.zeros((3, 6), dtype=torch.int32)[:, :4]) == 6
+    assert stride(one.expand(3, 4)) == 0
+    assert _call("hs_kv4_mqa_decode", DECODE, dict(stride=0)) == INV
+
+
 def test_page_bytes():
     assert hs.kv4_page_bytes(32, 16) == 16 * 20
     assert hs.kv4_page_bytes(512, 64) == 64 * (256 + 16)  # 4.25 bits an element
