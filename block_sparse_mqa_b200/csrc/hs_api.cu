@@ -864,6 +864,11 @@ hs_status hs_kv4_mqa_decode(const void* q, int64_t q_row_stride, int64_t q_head_
     return fail(HS_ERR_INVALID_ARG, "window %d or num_first %d < 0", window, num_first);
   if (window == 0 && num_first != 0)
     return fail(HS_ERR_INVALID_ARG, "num_first without a window");
+  // the kernels count the batch's tiles of 128 keys in 31 bits
+  const int64_t keys = window > 0 ? std::min((int64_t)max_seqlen, (int64_t)window + num_first) : max_seqlen;
+  if ((keys + 127) / 128 * num_seqs > INT32_MAX)
+    return fail(HS_ERR_UNSUPPORTED, "num_seqs %d times %lld keys is more than one call takes", num_seqs,
+                (long long)keys);
   if (!aligned16(k_cache) || !aligned16(v_cache))
     return fail(HS_ERR_INVALID_ARG, "a cache is not 16-byte aligned");
   if (num_seqs == 0) return HS_OK;

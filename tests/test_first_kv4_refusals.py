@@ -76,7 +76,8 @@ def test_read_refuses(kw, code):
     (dict(q=None), INV), (dict(kc=None), INV), (dict(out=None), INV), (dict(lse=None), INV), (dict(maxlen=0), INV),
     (dict(vc=None, dv=608), INV), (dict(qhs=100), INV), (dict(qrs=576), INV), (dict(scale=float("inf")), INV),
     (dict(window=-1), INV), (dict(first=-1), INV), (dict(first=3), INV), (dict(kc=264), INV), (dict(vc=264), INV),
-    (dict(ws=None), WSP), (dict(wsb=16), WSP), (dict(ws=264), INV), (dict(S=2 ** 30), UNS)])
+    (dict(ws=None), WSP), (dict(wsb=16), WSP), (dict(ws=264), INV), (dict(S=2 ** 30), UNS),
+    (dict(S=129, maxlen=2 ** 31 - 1), UNS), (dict(S=2 ** 20, maxlen=2 ** 31 - 1, window=2 ** 20, first=1), UNS)])
 def test_decode_refuses(kw, code):
     assert _call("hs_kv4_mqa_decode", DECODE, kw) == code
 
