@@ -313,6 +313,31 @@ def test_gradients_at_any_element(which):
         assert bool((h[:off] == 7).all()) and bool((h[off + grads[i].numel():] == 7).all())
 
 
+def test_far_tokens_pass_32_bit_offsets():
+    """70000 tokens of the MLA shape, where out, q and the gradients have more than
+    2^31 elements: the last rows and keys, and the first tokens' share in them."""
+    T, W, F, n = 70000, 100, 4, 300
+    g = torch.Generator(device=DEV)
+    g.manual_seed(18)
+    new = lambda *shape: torch.randn(shape, generator=g, device=DEV, dtype=BF16)
+    q, k, v, dout, sink = new(T, 64, 576), new(T, 576), new(T, 512), new(T, 64, 512), new(64).float()
+    args = (torch.tensor([0, T], device=DEV, dtype=torch.int32), T, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(q, k, v, *args, sink)
+    grads = hs.hs_swa_first_mqa_bwd(q, k, v, *args, out, lse, dout, sink)
+    hs.poll_status()
+    rows = slice(T - n, T)
+    keys = torch.cat([torch.arange(F, device=DEV), torch.arange(T - n - W, T, device=DEV)])
+    t = torch.arange(T - n, T, device=DEV)[:, None]
+    mask = (keys <= t) & ((keys > t - W) | (keys < F))
+    ref, rlse, bo, bl = A.forward(q[rows], k[keys], v[keys], mask, sink, 576 ** -0.5, BF16)
+    A.check(out[rows], ref, bo, "out")
+    A.check(lse[rows], rlse, bl, "lse")
+    ref = A.backward(q[rows], k[keys], v[keys], out[rows], lse[rows], dout[rows], mask, None, 576 ** -0.5, BF16)
+    A.check(grads[0][rows], *ref["dq"], "dq")
+    for i, name in ((1, "dk"), (2, "dv")):  # keys that only these rows attend
+        A.check(grads[i][rows], *(x[F + W:] for x in ref[name]), name)
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
