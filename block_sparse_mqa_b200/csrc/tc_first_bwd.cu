@@ -522,8 +522,14 @@ namespace pb {
 
 constexpr int kThreads = 256;   // warp 0 producer, warp 1 issuer, warps 4..7 epilogue
 constexpr int kKeys = 256;      // keys of a window item
-// Tokens of an item: many make few partial sums, few keep every SM busy.
-__host__ __device__ constexpr int tok_of(int T) { return T >= 2048 ? 128 : T >= 1024 ? 64 : 32; }
+// Tokens of an item: many make few partial sums, few keep every SM busy.  Whole
+// backward at window 512 + 4, MLA shape, us with 32 / 64 / 128 / 256 tokens:
+//   T 150: 68 / 84 / 120      T 420: 147 / 131 / 165     T 600: 222 / 217 / 205
+//   T 2047: 693 / 611 / 589   T 4096: 1402 / 1247 / 1180 / 1145   T 8192: - / - / 2462 / 2319
+// (window 128: T 4096 731 with 128, 774 with 256; T 16384 2944 and 2871).
+__host__ __device__ constexpr int tok_of(int T) {
+  return T >= 5000 ? 256 : T >= 560 ? 128 : T >= 350 ? 64 : 32;
+}
 constexpr int kStages = 4;
 constexpr int kPanel = 8192;    // 64 heads x 64 columns
 constexpr int kStageBytes = 6 * kPanel;  // 4 panels of q or dout, 2 of the band

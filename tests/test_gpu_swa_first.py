@@ -313,6 +313,26 @@ def test_gradients_at_any_element(which):
         assert bool((h[:off] == 7).all()) and bool((h[off + grads[i].numel():] == 7).all())
 
 
+def test_many_tokens_in_several_documents():
+    """Enough tokens for the backward's longest items, each document checked by itself."""
+    docs, W, F = [1300, 3, 1250, 1100, 1290, 260], 70, 9
+    inp, dout = _inputs(docs, 64, 64, 128, BF16, 19)
+    cu = inp.cu_seqlens.tolist()
+    args = (inp.cu_seqlens, 1300, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink)
+    hs.poll_status()
+    for bos, eos in zip(cu, cu[1:]):
+        r = slice(bos, eos)
+        mask = A.mask_of([0, eos - bos], W, F, DEV)
+        ref, rlse, bo, bl = A.forward(inp.q[r], inp.k[r], inp.v[r], mask, inp.sink, 64 ** -0.5, BF16)
+        A.check(out[r], ref, bo, "out")
+        A.check(lse[r], rlse, bl, "lse")
+        ref = A.backward(inp.q[r], inp.k[r], inp.v[r], out[r], lse[r], dout[r], mask, None, 64 ** -0.5, BF16)
+        for x, name in zip(g, ("dq", "dk", "dv")):
+            A.check(x[r], *ref[name], name)
+
+
 def test_far_tokens_pass_32_bit_offsets():
     """70000 tokens of the MLA shape, where out, q and the gradients have more than
     2^31 elements: the last rows and keys, and the first tokens' share in them."""
