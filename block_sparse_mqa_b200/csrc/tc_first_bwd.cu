@@ -27,6 +27,15 @@
 //           the same q and dout from L2 (each token meets three key tiles).
 //   reduce  adds a key's partial sums in order, scales, rounds once
 // Results are deterministic.  All waits are bounded (HS_ERR_TIMEOUT).
+//
+// Measured (Dk 576 / Dv 512, 4096 tokens, window 512 + 4 first, in a graph): the
+// whole backward 1.18 ms, 590 TFLOP/s, 0.36 of a cuBLAS matmul's rate (delta 90
+// us, pass A 0.61 ms, pass B 0.44 ms, reduce 45 us); the passes of
+// tc_bwd_dq.cu and tc_bwd_dkdv.cu, which recompute P and dS for dk and dv and
+// take one token per CTA, need 3.81 ms for the same and less workspace (333
+// tokens, window 64 + 5: 321 us for 105).
+// Pass A is bound by its S and dP MMAs (N = 128: ~91 cycles each from one issuing
+// warp) and its loads, pass B by q, dout and the band out of L2 and DRAM.
 
 #include <math.h>
 

@@ -36,6 +36,13 @@
 // and a second kernel that joins them in order (deterministic).  A CTA has at
 // most two partial sequences, its first and its last.
 // All waits are bounded (HS_ERR_TIMEOUT).
+//
+// Measured (64 heads, Dk 576 / Dv 512 in one plane, in a graph): 64 sequences of
+// ~4900 keys 81 us, 540 TFLOP/s and 1.3 TB/s; 4 sequences of 65536 keys at most 92 us.  A
+// tile of 128 keys costs ~6.3K cycles (PV 1.7K, then expansion, QK and softmax
+// behind one another in part); ~20 us are prologue, epilogue and the join.
+// The CUDA-core kernel takes 353 us for 8 sequences of 2048 keys at most that
+// take 23 us here, and 39 us for one of 777 that takes 18.
 
 #include <math.h>
 
