@@ -20,20 +20,21 @@
 // need no case of their own.
 //   pass A  per pair of tokens, tiles of 128 keys: S = Q K^T, dP = dO V^T,
 //           P and dS to the band, dQ += dS K                   (M = 128)
-//   pass B  per (tok tokens, 256 keys, 512 columns of dk or dv): partial
+//   pass B  per (tok tokens, up to 256 of the keys that their windows reach,
+//           512 columns of dk or dv): partial
 //           dV^T += dO^T P or dK^T += Q^T dS                   (M = 256, N = 256)
 //           and the same per (tok tokens of a document, its first tokens).
 //           Items go by their tokens, so that the ones running together read
-//           the same q and dout from L2 (each token meets three key tiles).
+//           the same q and dout from L2.
 //   reduce  adds a key's partial sums in order, scales, rounds once
 // Results are deterministic.  All waits are bounded (HS_ERR_TIMEOUT).
 //
 // Measured (Dk 576 / Dv 512, 4096 tokens, window 512 + 4 first, in a graph): the
-// whole backward 1.18 ms, 590 TFLOP/s, 0.36 of a cuBLAS matmul's rate (delta 90
-// us, pass A 0.61 ms, pass B 0.44 ms, reduce 45 us); the passes of
+// whole backward 1.14 ms, 612 TFLOP/s, 0.37 of a cuBLAS matmul's rate (delta 77
+// us, pass A 0.61 ms, pass B and the reduction the rest); the passes of
 // tc_bwd_dq.cu and tc_bwd_dkdv.cu, which recompute P and dS for dk and dv and
 // take one token per CTA, need 3.81 ms for the same and less workspace (333
-// tokens, window 64 + 5: 321 us for 105).
+// tokens, window 64 + 5: 321 us for 77).
 // Pass A is bound by its S and dP MMAs (N = 128: ~91 cycles each from one issuing
 // warp) and its loads, pass B by q, dout and the band out of L2 and DRAM.
 
@@ -530,15 +531,14 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
 namespace pb {
 
 constexpr int kThreads = 256;   // warp 0 producer, warp 1 issuer, warps 4..7 epilogue
-constexpr int kKeys = 256;      // keys of a window item
-// Tokens of an item: many make few partial sums, few keep every SM busy.  Whole
-// backward at window 512 + 4, MLA shape, us with 32 / 64 / 128 / 256 tokens:
-//   T 150: 68 / 84 / 120      T 420: 147 / 131 / 165     T 600: 222 / 217 / 205
-//   T 2047: 693 / 611 / 589   T 4096: 1402 / 1247 / 1180 / 1145   T 8192: - / - / 2462 / 2319
-// (window 128: T 4096 731 with 128, 774 with 256; T 16384 2944 and 2871).
-__host__ __device__ constexpr int tok_of(int T) {
-  return T >= 5000 ? 256 : T >= 560 ? 128 : T >= 350 ? 64 : 32;
-}
+constexpr int kKeys = 256;      // most keys of an item
+// Tokens of an item: many make few partial sums and a small workspace, few keep
+// every SM busy.  Whole backward at the MLA shape, us with 32 / 64 / 128 / 256 tokens:
+//   window 512 + 4: T 150: 64 / 83 / 93 / 124       T 420: 148 / 130 / 146 / 235
+//     T 1023: 308 / 294 / 311 / 340                 T 4096: 1220 / 1140 / 1146 / 1157
+//     T 8192: 2469 / 2352 / 2335 / 2400
+//   window 64 + 5, T 333: 77 / 89 / 123 / 126       window 128 + 4, T 4096: 699 / 679 / 683 / 697
+__host__ __device__ constexpr int tok_of(int T) { return T >= 8192 ? 128 : T >= 400 ? 64 : 32; }
 constexpr int kStages = 4;
 constexpr int kPanel = 8192;    // 64 heads x 64 columns
 constexpr int kStageBytes = 6 * kPanel;  // 4 panels of q or dout, 2 of the band
@@ -548,9 +548,9 @@ struct Params {
   Band band;
   int dk, dv;
   int gk, groups;     // 512-column groups of Dk; of Dk and Dv together
-  int tiles, parts;   // key tiles; token parts of a tile
+  int segs, n;        // items of a chunk's keys, each n of them
   int tok, chunks;    // tokens of an item; as many chunks of them in the batch
-  float* wpart;       // [tiles][parts][kKeys][dk + dv]
+  float* wpart;       // [chunks][segs * n][dk + dv]
   float* fpart;       // [chunks + num_docs][fp][dk + dv]
   int* status;
   long long wait_ns;
@@ -579,10 +579,9 @@ struct Jobs {
   __device__ __forceinline__ Jobs(const Params& pp, int first, int pairs)
       : p(pp), item(first), step(pairs), doc_t(-1) {}
   __device__ __forceinline__ bool next(Job& j) {
-    // chunk by chunk of tokens: the key tiles it meets (from its own backwards),
-    // the column groups of each
-    const int per = kKeys / p.tok, meets = (p.parts + per - 1) / per;
-    const int nwin = p.chunks * meets * p.groups;
+    // chunk by chunk of tokens, c0 ..: its keys from c0 - Wp, the column groups of
+    // each
+    const int nwin = p.chunks * p.segs * p.groups;
     const int total = nwin + (p.band.fp > 0 ? p.chunks * p.groups : 0);
     const int W = p.dk + p.dv;
     for (; item < total; item += step) {
@@ -595,17 +594,16 @@ struct Jobs {
       j.cols = min(512, (j.is_k ? p.dk : p.dv) - j.col0);
       const int at = (j.is_k ? 0 : p.dk) + j.col0;
       if (item < nwin) {
-        const int chunk = r / meets, tile = chunk / per - r % meets, part = chunk - tile * per;
-        if (tile < 0 || part >= p.parts) continue;
-        r = tile * p.parts + part;
+        const int c0 = r / p.segs * p.tok;
         j.window = true;
-        j.key0 = tile * kKeys;
-        j.n = kKeys;
-        j.t0 = chunk * p.tok;
-        j.t1 = min(min(j.t0 + p.tok, p.d.T), j.key0 + kKeys - 1 + p.band.window);
+        j.key0 = c0 - p.band.wp + r % p.segs * p.n;
+        j.n = p.n;
+        // tokens whose windows reach these keys
+        j.t0 = max(c0, j.key0);
+        j.t1 = min(min(c0 + p.tok, p.d.T), j.key0 + p.n - 1 + p.band.window);
         if (j.t0 >= j.t1) continue;
-        j.dst = p.wpart + (int64_t)r * kKeys * W + at;
-        j.keys = min(kKeys, p.d.T - j.key0);
+        j.dst = p.wpart + (int64_t)r * p.n * W + at;
+        j.keys = min(p.n, p.d.T - j.key0);
         item += step;
         return true;
       }
@@ -794,16 +792,14 @@ key_pass(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
   if (warp == 1) tmem_dealloc_pair(tmem, 512);
 }
 
-// dk and dv of one key: its partial sums in order.  The ones that no job wrote
-// (no token in them) are left out by the jobs' own rule.
+// dk and dv of one key: its partial sums in order, only ones that a job wrote.
 __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, float scale,
                                               __nv_bfloat16* dkey, __nv_bfloat16* dval,
                                               int* spoiled) {
   const int W = p.dk + p.dv;
   for (int j = blockIdx.x; j < p.d.T; j += gridDim.x) {
-    const int tile = j / kKeys, key0 = tile * kKeys;
-    const int tend = min(p.d.T, key0 + kKeys - 1 + p.band.window);
-    const int parts = min(p.parts, (tend - key0 + p.tok - 1) / p.tok);
+    // chunks with a token whose window reaches j
+    const int w0 = j / p.tok, w1 = min(p.d.T - 1, j + p.band.window - 1) / p.tok;
     int bos, eos, doc = 0, c0 = 1, c1 = 0, f = 0;  // chunks with first-token sums
     if (p.band.fp > 0 &&
         find_doc(p.d.cu, p.d.num_docs, p.d.T, p.d.max_seqlen, j, bos, eos, nullptr)) {
@@ -828,8 +824,8 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
         s.z += v.z;
         s.w += v.w;
       };
-      for (int q = 0; q < parts; ++q)
-        add(p.wpart + (((int64_t)tile * p.parts + q) * kKeys + (j - key0)) * W + col);
+      for (int c = w0; c <= w1; ++c)
+        add(p.wpart + ((int64_t)c * p.segs * p.n + (j - (c * p.tok - p.band.wp))) * W + col);
       for (int c = c0; c <= c1; ++c)
         add(p.fpart + ((int64_t)(c + doc) * p.band.fp + f) * W + col);
       const bool is_k = col < p.dk;
@@ -853,17 +849,18 @@ int64_t band_stride(int64_t span) { return (span + 51) & ~(int64_t)7; }
 
 struct Sizes {
   size_t band, wpart, fpart;
-  int tiles, parts, chunks;
+  int chunks, segs, n;
 };
 Sizes sizes_of(int T, int num_docs, int span, int window, int fp, int dk, int dv) {
   Sizes z{};
   const size_t W = (size_t)(dk + dv) * sizeof(float);
   z.band = align256((size_t)T * kH * band_stride(span) * 2);
-  z.tiles = (T + pb::kKeys - 1) / pb::kKeys;
   const int tok = pb::tok_of(T);
-  z.parts = (pb::kKeys - 1 + window + tok - 1) / tok;
+  const int keys = ((window - 1 + 7) & ~7) + tok;  // of a chunk
   z.chunks = (T + tok - 1) / tok;
-  z.wpart = align256((size_t)z.tiles * z.parts * pb::kKeys * W);
+  z.segs = (keys + pb::kKeys - 1) / pb::kKeys;
+  z.n = ((keys + z.segs - 1) / z.segs + 31) & ~31;
+  z.wpart = align256((size_t)z.chunks * z.segs * z.n * W);
   z.fpart = align256((size_t)(z.chunks + num_docs) * fp * W);
   return z;
 }
@@ -954,8 +951,8 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   k.dv = p.dv;
   k.gk = (p.dk + 511) / 512;
   k.groups = k.gk + (p.dv + 511) / 512;
-  k.tiles = z.tiles;
-  k.parts = z.parts;
+  k.segs = z.segs;
+  k.n = z.n;
   k.tok = pb::tok_of(T);
   k.chunks = z.chunks;
   k.wpart = reinterpret_cast<float*>(w + 2 * z.band);
