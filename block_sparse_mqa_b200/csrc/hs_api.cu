@@ -118,13 +118,14 @@ hs_status check_problem(hs::Problem& p, const void* q, int64_t qrs, int64_t qhs,
 // The backward's workspace: the delta / sink terms of every path, then (for
 // shapes the tensor-core passes take) the dk / dv pass's partial sums at a
 // 256-byte boundary.
-size_t bwd_simt_bytes(int total_tokens, int num_heads) {
-  return (hs::simt_backward_workspace(total_tokens, num_heads) + 255) & ~(size_t)255;
+size_t bwd_simt_bytes(int total_tokens, int num_heads, bool with_first) {
+  const size_t flags = with_first ? 2 * sizeof(int) * (size_t)total_tokens : 0;
+  return (hs::simt_backward_workspace(total_tokens, num_heads) + flags + 255) & ~(size_t)255;
 }
 // span > 0: the window attention with first tokens, window + first keys.
 size_t bwd_workspace(int total_tokens, int num_heads, int dk, int dv, hs_dtype dtype,
                      int num_docs = 0, int max_seqlen = 0, int span = 0) {
-  size_t need = bwd_simt_bytes(total_tokens, num_heads);
+  size_t need = bwd_simt_bytes(total_tokens, num_heads, span > 0);
   if (!g_force_simt.load() && hs::tc_backward_shape_ok(dtype, num_heads, dk, dv)) {
     size_t tc = hs::tc_bwd_dkdv_workspace(total_tokens, dk, dv);
     if (span > 0)
@@ -606,10 +607,9 @@ static hs_status backward_common(hs::BwdArgs& a, bool sparse, const void* q, int
   if ((reinterpret_cast<uintptr_t>(workspace) & 15) != 0)
     return fail(HS_ERR_INVALID_ARG, "workspace is not 16-byte aligned");
   a.workspace = workspace;
-  a.dkdv_ws = need > bwd_simt_bytes(total_tokens, num_heads)
-                  ? static_cast<char*>(workspace) + bwd_simt_bytes(total_tokens, num_heads)
-                  : nullptr;
-  a.dkdv_bytes = need - bwd_simt_bytes(total_tokens, num_heads);
+  const size_t own = bwd_simt_bytes(total_tokens, num_heads, a.with_first);
+  a.dkdv_ws = need > own ? static_cast<char*>(workspace) + own : nullptr;
+  a.dkdv_bytes = need - own;
   r = status_ptr(&a.p.status);
   if (r != HS_OK) return r;
   int path = HS_PATH_SIMT;

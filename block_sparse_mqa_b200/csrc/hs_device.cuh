@@ -53,6 +53,29 @@ __device__ __forceinline__ __nv_bfloat16 from_f32<__nv_bfloat16>(float x) {
   return __float2bfloat16_rn(x);
 }
 
+// A kernel that launch_after() started beside the end of the one before it in the
+// stream calls this before it touches memory (all of its threads, so that its own
+// end means the end of all before it), and lets the next one start early.
+__device__ __forceinline__ void after_previous() {
+  cudaGridDependencySynchronize();
+  cudaTriggerProgrammaticLaunchCompletion();
+}
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kern)(P...), unsigned grid, unsigned block, size_t smem,
+                         cudaStream_t s, const A&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
 // Warp reductions.
 __device__ __forceinline__ float warp_max(float v) {
 #pragma unroll

@@ -105,8 +105,11 @@ bool tc_first_eligible(const Problem& p);
 // them out.
 size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, int span, int dk,
                               int dv);
-cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled,
-                                int* spoiled_keys, void* ws, size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s);
+// dsink_part [T, H]: the sink terms that dsink sums.  The first of its kernels
+// goes before the end of the stream's last one (launch_after).
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, const float* dsink_part,
+                                int* spoiled, int* spoiled_keys, void* ws, size_t ws_bytes,
+                                long long wait_limit, bool* taken, cudaStream_t s);
 cudaError_t launch_tc_first_fwd(const AttnArgs& a, long long wait_limit, cudaStream_t s);
 size_t simt_backward_workspace(int total_tokens, int num_heads);
 // *path (may be null) receives the kernel family the dq and dk / dv passes use.

@@ -53,6 +53,7 @@ struct BwdParams {
   float* dsink_part;  // workspace [T, H]
   int G, KT;          // heads per group, keys per dq tile
   const int* only;    // the tokens (or keys) with only[t] != 0 alone (null: all)
+  int* flags;         // with_first: workspace [2, T], cleared with delta
 };
 
 template <typename T>
@@ -100,6 +101,7 @@ __global__ void __launch_bounds__(kThreads) bwd_delta_kernel(const BwdParams a) 
     a.delta[(int64_t)t * H + h] = acc;
     a.dsink_part[(int64_t)t * H + h] =
         a.sink ? -expf(__ldg(a.sink + h) - __ldg(a.lse + (int64_t)t * H + h)) * acc : 0.f;
+    if (a.flags && h == 0) a.flags[t] = a.flags[(int64_t)a.p.total_tokens + t] = 0;
   }
 }
 
@@ -108,6 +110,7 @@ __global__ void __launch_bounds__(kThreads) bwd_delta_kernel(const BwdParams a) 
 __global__ void __launch_bounds__(kThreads) bwd_delta16_kernel(const BwdParams a) {
   const int64_t th = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31, dv = a.p.dv, units = dv / 8;
+  cudaTriggerProgrammaticLaunchCompletion();  // what comes next waits for the end
   if (th >= (int64_t)a.p.total_tokens * a.p.num_heads) return;
   const uint4* const o = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.out) + th * dv);
   const uint4* const d = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.dout) + th * dv);
@@ -128,11 +131,15 @@ __global__ void __launch_bounds__(kThreads) bwd_delta16_kernel(const BwdParams a
     const int h = (int)(th % a.p.num_heads);
     a.delta[th] = acc;
     a.dsink_part[th] = a.sink ? -expf(__ldg(a.sink + h) - __ldg(a.lse + th)) * acc : 0.f;
+    if (h == 0) {
+      const int64_t t = th / a.p.num_heads;
+      a.flags[t] = a.flags[a.p.total_tokens + t] = 0;
+    }
   }
 }
 
 // ---------------------------------------------------------------- dsink
-__global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a) {
+__global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a, float* dsink) {
   __shared__ float red[kThreads];
   const int h = blockIdx.x, H = a.p.num_heads;
   float acc = 0.f;
@@ -144,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a) 
     if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
     __syncthreads();
   }
-  if (threadIdx.x == 0) a.dsink[h] = red[0];
+  if (threadIdx.x == 0) dsink[h] = red[0];
 }
 
 // ---------------------------------------------------------------- dq
@@ -163,7 +170,7 @@ __device__ __forceinline__ bool any_listed(const BwdParams& a) {
   int any = 0;
   for (int64_t t = blockIdx.x + (int64_t)threadIdx.x * gridDim.x; t < a.p.total_tokens;
        t += (int64_t)blockDim.x * gridDim.x)
-    any |= __ldg(a.only + t);
+    any |= a.only[t];
   return __syncthreads_or(any);
 }
 
@@ -185,9 +192,10 @@ __global__ void __launch_bounds__(kThreads) bwd_dq_kernel(const BwdParams a) {
   float* del_s = lse_s + G;
   int* blist = reinterpret_cast<int*>(del_s + G);
   const float scale = P.scale;
+  after_previous();
   if (a.only && !any_listed(a)) return;
   for (int t = blockIdx.x; t < P.total_tokens; t += gridDim.x) {
-    if (a.only && __ldg(a.only + t) == 0) continue;
+    if (a.only && a.only[t] == 0) continue;
     int bos, eos;
     if (!find_doc(P.cu_seqlens, P.num_docs, P.total_tokens, P.max_seqlen, t, bos, eos,
                   P.status))
@@ -457,9 +465,10 @@ __global__ void __launch_bounds__(kWarps * 32) bwd_key_kernel(const BwdParams a)
   const Problem& P = a.p;
   const int H = P.num_heads, dk = P.dk, dv = P.dv;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  after_previous();
   if (a.only && !any_listed(a)) return;
   for (int j = blockIdx.x; j < P.total_tokens; j += gridDim.x) {
-    if (a.only && __ldg(a.only + j) == 0) continue;
+    if (a.only && a.only[j] == 0) continue;
     int bos, eos;
     if (!find_doc(P.cu_seqlens, P.num_docs, P.total_tokens, P.max_seqlen, j, bos, eos, P.status))
       continue;
@@ -540,13 +549,9 @@ template <typename T>
 cudaError_t launch_keys(const BwdParams& a, cudaStream_t s) {
   const int most = a.p.dk > a.p.dv ? a.p.dk : a.p.dv;
   const int grid = a.only && a.p.total_tokens > 148 ? 148 : a.p.total_tokens;
-  if (most <= 64)
-    bwd_key_kernel<T, 2, 2, 16><<<grid, 512, 0, s>>>(a);
-  else if (most <= 256)
-    bwd_key_kernel<T, 8, 8, 16><<<grid, 512, 0, s>>>(a);
-  else
-    bwd_key_kernel<T, 32, 32, 8><<<grid, 256, 0, s>>>(a);
-  return cudaGetLastError();
+  if (most <= 64) return launch_after(bwd_key_kernel<T, 2, 2, 16>, grid, 512, 0, s, a);
+  if (most <= 256) return launch_after(bwd_key_kernel<T, 8, 8, 16>, grid, 512, 0, s, a);
+  return launch_after(bwd_key_kernel<T, 32, 32, 8>, grid, 256, 0, s, a);
 }
 
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -568,8 +573,7 @@ cudaError_t launch_dq(BwdParams a, cudaStream_t s) {
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e != cudaSuccess) return e;
   const int grid = a.only && P.total_tokens > 148 ? 148 : P.total_tokens;
-  kern<<<grid, kThreads, bytes, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(kern, grid, kThreads, bytes, s, a);
 }
 
 template <typename T, bool kSparse>
@@ -579,6 +583,7 @@ cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
   const int pairs = NT * H;
   const unsigned blocks = (unsigned)((pairs + kThreads / 32 - 1) / (kThreads / 32));
   const bool wide = a.with_first && P.dtype == HS_BF16 && P.dv % 8 == 0 &&
+                    a.flags != nullptr &&
                     ((reinterpret_cast<uintptr_t>(a.out) | reinterpret_cast<uintptr_t>(a.dout)) & 15) == 0;
   if (wide)
     bwd_delta16_kernel<<<blocks, kThreads, 0, s>>>(a);
@@ -587,7 +592,7 @@ cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.dsink && a.sink) {
-    bwd_dsink_kernel<<<H, kThreads, 0, s>>>(a);
+    bwd_dsink_kernel<<<H, kThreads, 0, s>>>(a, a.dsink);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -643,6 +648,9 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
   a.with_first = b.with_first;
   a.delta = static_cast<float*>(b.workspace);
   a.dsink_part = a.delta + (size_t)b.p.total_tokens * b.p.num_heads;
+  a.flags = b.with_first
+                ? reinterpret_cast<int*>(a.dsink_part + (size_t)b.p.total_tokens * b.p.num_heads)
+                : nullptr;
   if (b.p.dtype == HS_BF16) {
     // tensor cores: dq and dk / dv on tcgen05 (else every pass on CUDA cores)
     auto al16 = [](const void* x) { return (reinterpret_cast<uintptr_t>(x) & 15) == 0; };
@@ -651,30 +659,29 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
                      // bf16 gradients are stored 16 and 4 bytes at a time
                      (!b.grad_like_input || (al16(b.dq) && al16(b.dkey) && al16(b.dval)));
     if (path) *path = mma ? HS_PATH_MMA : HS_PATH_SIMT;
+    if (mma && b.with_first) a.dsink = nullptr;  // below
     cudaError_t e = sparse ? launch_typed<__nv_bfloat16, true>(a, !mma, s)
                            : launch_typed<__nv_bfloat16, false>(a, !mma, s);
     if (e != cudaSuccess || !mma) return e;
     // With visible first tokens nothing outside the key sets may show: a dq
     // that a key outside spoiled, and a dk or dv that a query outside spoiled
-    // (0 * NaN in a whole-tile product), is flagged and computed again.  The
-    // sink terms' place (64 heads) is free for both flags.
-    const size_t nt = (size_t)b.p.total_tokens;
-    int* const flags = b.with_first ? reinterpret_cast<int*>(a.dsink_part) : nullptr;
-    int* const kflags = flags ? flags + nt : nullptr;
-    if (flags) {
-      e = cudaMemsetAsync(flags, 0, 2 * sizeof(int) * nt, s);
-      if (e != cudaSuccess) return e;
-    }
+    // (0 * NaN in a whole-tile product), is flagged and computed again.
+    int* const flags = a.flags;
+    int* const kflags = flags ? flags + (size_t)b.p.total_tokens : nullptr;
     bool taken = false;  // the window's own passes, where their workspace was given
     if (flags) {
-      e = launch_tc_first_bwd(b, a.delta, flags, kflags, b.dkdv_ws, b.dkdv_bytes, 0, &taken, s);
+      e = launch_tc_first_bwd(b, a.delta, a.dsink_part, flags, kflags, b.dkdv_ws, b.dkdv_bytes, 0,
+                              &taken, s);
       if (e != cudaSuccess) return e;
     }
     if (!taken) {
+      if (flags && b.dsink && b.sink) {
+        bwd_dsink_kernel<<<b.p.num_heads, kThreads, 0, s>>>(a, b.dsink);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+      }
       e = launch_tc_bwd_dq(b, sparse, a.delta, flags, 0, s);
       if (e != cudaSuccess) return e;
-    }
-    if (!taken) {
       e = launch_tc_bwd_dkdv(b, sparse, a.delta, kflags, 0, s);
       if (e != cudaSuccess) return e;
     }

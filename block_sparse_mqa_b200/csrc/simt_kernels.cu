@@ -261,6 +261,7 @@ simt_attention_kernel(AttnArgs a) {
 __global__ void __launch_bounds__(kAttnThreads) simt_redo_kernel(AttnArgs a) {
   extern __shared__ float smem[];
   __shared__ int marked[kAttnThreads];
+  after_previous();
   const int64_t n = (int64_t)a.p.total_tokens * a.p.num_heads;
   for (int64_t base = (int64_t)blockIdx.x * kAttnThreads; base < n;
        base += (int64_t)gridDim.x * kAttnThreads) {
@@ -304,8 +305,8 @@ cudaError_t launch_simt_redo(const AttnArgs& a, cudaStream_t s) {
   if (a.p.dv > kAttnThreads * kMaxDvPerThread) return cudaErrorInvalidValue;
   const int64_t blocks = ((int64_t)a.p.total_tokens * a.p.num_heads + kAttnThreads - 1) / kAttnThreads;
   const size_t smem = sizeof(float) * ((size_t)a.p.dk + 128 + 32);
-  simt_redo_kernel<<<(unsigned)(blocks < 592 ? blocks : 592), kAttnThreads, smem, s>>>(a);
-  return cudaGetLastError();
+  return launch_after(simt_redo_kernel, (unsigned)(blocks < 592 ? blocks : 592), kAttnThreads, smem,
+                      s, a);
 }
 
 cudaError_t launch_simt_attention(const AttnArgs& a, bool sparse, cudaStream_t s) {

@@ -197,6 +197,7 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  after_previous();
   const uint32_t tmem = sh->tmem_base;
   Walk walk(p.d, blockIdx.x >> 1, gridDim.x >> 1);
   Pass ps;
@@ -224,7 +225,7 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       float lse2 = 0.f, del = 0.f;
       if (act) {
         lse2 = __ldg(p.lse + th) * kLog2e;
-        del = __ldg(p.delta + th);
+        del = p.delta[th];
       }
       for (int i = 0; i < tl.count() && ok; ++i) {
         const int n2 = tl.n(i) / 2, c0 = 32 * ch, k0 = hi * n2 + c0;  // key of column 0 in the tile
@@ -672,6 +673,7 @@ key_pass(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
   __syncthreads();
   cluster_sync();
   tc_fence_after();
+  after_previous();
   const uint32_t tmem = sh->tmem_base;
   Jobs jobs(p, blockIdx.x >> 1, gridDim.x >> 1);
   Job j;
@@ -793,11 +795,33 @@ key_pass(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUten
 }
 
 // dk and dv of one key: its partial sums in order, only ones that a job wrote.
-__global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, float scale,
+// A thread has 4 columns of each of its block's keys.  The first kH blocks sum the
+// sink's terms where dsink is wanted.
+constexpr int kReduce = 288;  // threads, at least (Dk + Dv) / 4
+__global__ void __launch_bounds__(kReduce) reduce(const __grid_constant__ Params p, float scale,
                                               __nv_bfloat16* dkey, __nv_bfloat16* dval,
-                                              int* spoiled) {
-  const int W = p.dk + p.dv;
-  for (int j = blockIdx.x; j < p.d.T; j += gridDim.x) {
+                                              int* spoiled, const float* dsink_part,
+                                              float* dsink) {
+  const int W = p.dk + p.dv, extra = dsink ? kH : 0;
+  after_previous();
+  if ((int)blockIdx.x < extra) {
+    __shared__ float red[256];
+    float acc = 0.f;
+    if (threadIdx.x < 256) {
+#pragma unroll 4
+      for (int t = threadIdx.x; t < p.d.T; t += 256)
+        acc += dsink_part[(int64_t)t * kH + blockIdx.x];
+      red[threadIdx.x] = acc;
+    }
+    __syncthreads();
+    for (int o = 128; o > 0; o >>= 1) {
+      if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
+      __syncthreads();
+    }
+    if (threadIdx.x == 0) dsink[blockIdx.x] = red[0];
+    return;
+  }
+  for (int j = blockIdx.x - extra; j < p.d.T; j += gridDim.x - extra) {
     // chunks with a token whose window reaches j
     const int w0 = j / p.tok, w1 = min(p.d.T - 1, j + p.band.window - 1) / p.tok;
     int bos, eos, doc = 0, c0 = 1, c1 = 0, f = 0;  // chunks with first-token sums
@@ -815,7 +839,8 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
         c1 = (eos - 1) / p.tok;
       }
     }
-    for (int col = threadIdx.x * 4; col < W; col += 1024) {
+    const int col = threadIdx.x * 4;
+    if (col < W) {
       float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
       auto add = [&](const float* at) {
         const float4 v = __ldcs(reinterpret_cast<const float4*>(at));
@@ -824,8 +849,10 @@ __global__ void __launch_bounds__(256) reduce(const __grid_constant__ Params p, 
         s.z += v.z;
         s.w += v.w;
       };
+#pragma unroll 4
       for (int c = w0; c <= w1; ++c)
         add(p.wpart + ((int64_t)c * p.segs * p.n + (j - (c * p.tok - p.band.wp))) * W + col);
+#pragma unroll 4
       for (int c = c0; c <= c1; ++c)
         add(p.fpart + ((int64_t)(c + doc) * p.band.fp + f) * W + col);
       const bool is_k = col < p.dk;
@@ -881,8 +908,9 @@ size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, in
   return n <= kMostBytes ? n : 0;
 }
 
-cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoiled,
-                                int* spoiled_keys, void* ws, size_t ws_bytes, long long wait_limit, bool* taken, cudaStream_t s) {
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, const float* dsink_part,
+                                int* spoiled, int* spoiled_keys, void* ws, size_t ws_bytes,
+                                long long wait_limit, bool* taken, cudaStream_t s) {
   *taken = false;
   const Problem& p = b.p;
   Band band;
@@ -940,9 +968,8 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   cudaError_t e = cudaFuncSetAttribute(pa::query_pass, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)pa::kSmem);
   if (e != cudaSuccess) return e;
-  pa::query_pass<<<pair_grid(T), pa::kThreads, pa::kSmem, s>>>(kmap, kmap16, vmap, vmap16, qmap,
-                                                              dmap, a);
-  e = cudaGetLastError();
+  e = launch_after(pa::query_pass, pair_grid(T), pa::kThreads, pa::kSmem, s, kmap, kmap16, vmap,
+                   vmap16, qmap, dmap, a);
   if (e != cudaSuccess) return e;
   pb::Params k{};
   k.d = a.d;
@@ -962,13 +989,13 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, int* spoil
   e = cudaFuncSetAttribute(pb::key_pass, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)pb::kSmem);
   if (e != cudaSuccess) return e;
-  pb::key_pass<<<2 * std::max(1, sm_count() / 2), pb::kThreads, pb::kSmem, s>>>(qmap, dmap, pw, pf,
-                                                                               sw, sf, k);
-  e = cudaGetLastError();
+  e = launch_after(pb::key_pass, 2 * std::max(1, sm_count() / 2), pb::kThreads, pb::kSmem, s, qmap,
+                   dmap, pw, pf, sw, sf, k);
   if (e != cudaSuccess) return e;
-  pb::reduce<<<std::min(T, 148 * 8), 256, 0, s>>>(k, p.scale, static_cast<__nv_bfloat16*>(b.dkey),
-                                                 static_cast<__nv_bfloat16*>(b.dval), spoiled_keys);
-  return cudaGetLastError();
+  float* const dsink = b.sink ? b.dsink : nullptr;
+  return launch_after(pb::reduce, std::min(T, 148 * 7) + (dsink ? kH : 0), pb::kReduce, 0, s, k, p.scale,
+                      static_cast<__nv_bfloat16*>(b.dkey), static_cast<__nv_bfloat16*>(b.dval),
+                      spoiled_keys, dsink_part, dsink);
 }
 
 }  // namespace hs

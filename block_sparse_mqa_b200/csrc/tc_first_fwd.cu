@@ -142,6 +142,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
   __syncthreads();
   cluster_sync();  // barriers of both CTAs exist
   tc_fence_after();
+  cudaTriggerProgrammaticLaunchCompletion();  // the check of the rows waits for the end
   const uint32_t tmem = sh->tmem_base;
   // registers: 512 threads launch with 128 each; 8 softmax warps take 168 and
   // the other two warpgroups give 48 each (8 * 168 + 8 * 80 <= 16 * 128)
