@@ -101,15 +101,16 @@ cudaError_t launch_simt_redo(const AttnArgs& a, cudaStream_t s);
 bool tc_first_shape_ok(hs_dtype dtype, int num_heads, int dk, int dv);
 bool tc_first_eligible(const Problem& p);
 // Bytes of the backward's passes for window + first = span keys (0: they do
-// not take it); *taken = false where the workspace or the first tokens rule
-// them out.
+// not take it).
 size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, int span, int dk,
                               int dv);
-// dsink_part [T, H]: the sink terms that dsink sums.  The first of its kernels
-// goes before the end of the stream's last one (launch_after).
-cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, const float* dsink_part,
-                                int* spoiled, int* spoiled_keys, void* ws, size_t ws_bytes,
-                                long long wait_limit, bool* taken, cudaStream_t s);
+// False where the workspace or the number of first tokens rule them out.
+bool tc_first_bwd_takes(const BwdArgs& b);
+// with_delta: they compute delta [T, H] and the sink terms (out 16-byte aligned)
+// and clear the flags; else delta's kernel came just before.
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, bool with_delta, float* delta, float* dsink_part,
+                                int* spoiled, int* spoiled_keys, long long wait_limit,
+                                cudaStream_t s);
 cudaError_t launch_tc_first_fwd(const AttnArgs& a, long long wait_limit, cudaStream_t s);
 size_t simt_backward_workspace(int total_tokens, int num_heads);
 // *path (may be null) receives the kernel family the dq and dk / dv passes use.

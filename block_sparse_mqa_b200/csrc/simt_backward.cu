@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads) bwd_delta16_kernel(const BwdParams a
 }
 
 // ---------------------------------------------------------------- dsink
-__global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a, float* dsink) {
+__global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a) {
   __shared__ float red[kThreads];
   const int h = blockIdx.x, H = a.p.num_heads;
   float acc = 0.f;
@@ -151,7 +151,7 @@ __global__ void __launch_bounds__(kThreads) bwd_dsink_kernel(const BwdParams a, 
     if (threadIdx.x < o) red[threadIdx.x] += red[threadIdx.x + o];
     __syncthreads();
   }
-  if (threadIdx.x == 0) dsink[h] = red[0];
+  if (threadIdx.x == 0) a.dsink[h] = red[0];
 }
 
 // ---------------------------------------------------------------- dq
@@ -592,7 +592,7 @@ cudaError_t launch_typed(BwdParams a, bool cuda_core_passes, cudaStream_t s) {
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   if (a.dsink && a.sink) {
-    bwd_dsink_kernel<<<H, kThreads, 0, s>>>(a, a.dsink);
+    bwd_dsink_kernel<<<H, kThreads, 0, s>>>(a);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
   }
@@ -659,27 +659,28 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
                      // bf16 gradients are stored 16 and 4 bytes at a time
                      (!b.grad_like_input || (al16(b.dq) && al16(b.dkey) && al16(b.dval)));
     if (path) *path = mma ? HS_PATH_MMA : HS_PATH_SIMT;
-    if (mma && b.with_first) a.dsink = nullptr;  // below
-    cudaError_t e = sparse ? launch_typed<__nv_bfloat16, true>(a, !mma, s)
-                           : launch_typed<__nv_bfloat16, false>(a, !mma, s);
-    if (e != cudaSuccess || !mma) return e;
     // With visible first tokens nothing outside the key sets may show: a dq
     // that a key outside spoiled, and a dk or dv that a query outside spoiled
     // (0 * NaN in a whole-tile product), is flagged and computed again.
     int* const flags = a.flags;
     int* const kflags = flags ? flags + (size_t)b.p.total_tokens : nullptr;
-    bool taken = false;  // the window's own passes, where their workspace was given
-    if (flags) {
-      e = launch_tc_first_bwd(b, a.delta, a.dsink_part, flags, kflags, b.dkdv_ws, b.dkdv_bytes, 0,
-                              &taken, s);
+    // the window's own passes, where their workspace was given
+    // and with delta in their query pass, if that has enough to do beside it (4096
+    // tokens: Dk 576 / Dv 512 window 192 702 -> 730 us, 256 808 -> 796, 512 1109 ->
+    // 1058; Dk 192 / Dv 128 window 512 619 -> 694, 1024 1045 -> 1022)
+    const bool own = mma && b.with_first && tc_first_bwd_takes(b);
+    const int64_t keys = (int64_t)b.window + b.first;
+    const bool with_delta = own && al16(b.out) && keys * b.p.dv >= 120000;
+    cudaError_t e = cudaSuccess;
+    if (own) a.dsink = nullptr;  // a part of their reduction
+    if (!with_delta)
+      e = sparse ? launch_typed<__nv_bfloat16, true>(a, !mma, s)
+                 : launch_typed<__nv_bfloat16, false>(a, !mma, s);
+    if (e != cudaSuccess || !mma) return e;
+    if (own) {
+      e = launch_tc_first_bwd(b, with_delta, a.delta, a.dsink_part, flags, kflags, 0, s);
       if (e != cudaSuccess) return e;
-    }
-    if (!taken) {
-      if (flags && b.dsink && b.sink) {
-        bwd_dsink_kernel<<<b.p.num_heads, kThreads, 0, s>>>(a, b.dsink);
-        e = cudaGetLastError();
-        if (e != cudaSuccess) return e;
-      }
+    } else {
       e = launch_tc_bwd_dq(b, sparse, a.delta, flags, 0, s);
       if (e != cudaSuccess) return e;
       e = launch_tc_bwd_dkdv(b, sparse, a.delta, kflags, 0, s);

@@ -19,7 +19,8 @@
 // columns left or right of the band read as 0, so documents and window edges
 // need no case of their own.
 //   pass A  per pair of tokens, tiles of 128 keys: S = Q K^T, dP = dO V^T,
-//           P and dS to the band, dQ += dS K                   (M = 128)
+//           P and dS to the band, dQ += dS K                   (M = 128); where
+//           the keys are many, delta of the next pair beside it
 //   pass B  per (tok tokens, up to 256 of the keys that their windows reach,
 //           512 columns of dk or dv): partial
 //           dV^T += dO^T P or dK^T += Q^T dS                   (M = 256, N = 256)
@@ -30,11 +31,11 @@
 // Results are deterministic.  All waits are bounded (HS_ERR_TIMEOUT).
 //
 // Measured (Dk 576 / Dv 512, 4096 tokens, window 512 + 4 first, in a graph): the
-// whole backward 1.14 ms, 612 TFLOP/s, 0.37 of a cuBLAS matmul's rate (delta 77
-// us, pass A 0.61 ms, pass B and the reduction the rest); the passes of
+// whole backward 1.06 ms, 659 TFLOP/s, 0.40 of a cuBLAS matmul's rate (pass A
+// with delta 0.61 ms, pass B 0.41 ms, reduction 33 us); the passes of
 // tc_bwd_dq.cu and tc_bwd_dkdv.cu, which recompute P and dS for dk and dv and
 // take one token per CTA, need 3.81 ms for the same and less workspace (333
-// tokens, window 64 + 5: 321 us for 77).
+// tokens, window 64 + 5: 321 us for 67).
 // Pass A is bound by its S and dP MMAs (N = 128: ~91 cycles each from one issuing
 // warp) and its loads, pass B by q, dout and the band out of L2 and DRAM.
 
@@ -77,14 +78,19 @@ struct Params {
   Docs d;
   Band band;
   int nck, ndc, nqb;   // 64-column chunks of Dk and Dv, 128-column blocks of Dk
-  int dk;
+  int dk, dv;
   float scale, scale_log2;
   const float* lse;
-  const float* delta;
+  const float* sink;          // may be null
+  const __nv_bfloat16* out;   // null: delta is there already
+  const __nv_bfloat16* dout;
+  float* delta;
+  float* dsink_part;
   __nv_bfloat16* pband;
   __nv_bfloat16* sband;
   __nv_bfloat16* dq;
   int* spoiled;
+  int* spoiled_keys;
   int* status;
   long long wait_ns;
 };
@@ -92,7 +98,8 @@ struct Params {
 struct Shared {
   uint64_t afull[kSlots], aempty[kSlots], bfull[kSlots], bempty[kSlots];
   uint64_t qfull[kMaxQC], qempty[kMaxQC], dfull[kMaxDC], dempty[kMaxDC];
-  uint64_t sdfull, sempty[2], dpempty, dsfull, dqdone, passdone, oempty, drain[2];
+  uint64_t sdfull, sempty[2], dpempty, dsfull, dqdone, passdone, oempty, drain[2], delfull[2];
+  float delta[2][kH];  // by pass parity
   uint32_t tmem_base;
 };
 constexpr size_t kSmem = (size_t)2 * kSlots * kSlot + (size_t)(kMaxQC + kMaxDC) * kQChunk + kDsBytes +
@@ -190,6 +197,8 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
     mbar_init(&sh->oempty, 8);  // 4 epilogue warps of each CTA
     mbar_init(&sh->drain[0], 1);
     mbar_init(&sh->drain[1], 1);
+    mbar_init(&sh->delfull[0], 4);  // the epilogue warps
+    mbar_init(&sh->delfull[1], 4);
     fence_barrier_init();
   }
   if (warp == kSWarp) tmem_alloc_pair(&sh->tmem_base, 512);
@@ -209,7 +218,7 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
     const int g4 = warp & 3, ch = warp >> 2, hi = g4 >> 1;
     const int row = 32 * (g4 & 1) + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * g4) << 16);
-    uint32_t nt = 0;  // live tiles
+    uint32_t nt = 0, npass = 0;  // live tiles
     auto tell_leader = [&](uint64_t* bar) {
       tc_fence_before();
       __syncwarp();
@@ -222,11 +231,10 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       const int own = max(ps.bos, t - p.band.window + 1);  // this token's window
       const int nf = min(p.band.first, own - ps.bos);      // and first tokens
       const int64_t th = (int64_t)t * kH + row;
-      float lse2 = 0.f, del = 0.f;
-      if (act) {
-        lse2 = __ldg(p.lse + th) * kLog2e;
-        del = p.delta[th];
-      }
+      const float lse2 = act ? __ldg(p.lse + th) * kLog2e : 0.f;
+      if (!warp_wait(&sh->delfull[npass & 1], (npass >> 1) & 1, lim)) { ok = false; break; }
+      const float del = sh->delta[npass & 1][row];
+      ++npass;
       for (int i = 0; i < tl.count() && ok; ++i) {
         const int n2 = tl.n(i) / 2, c0 = 32 * ch, k0 = hi * n2 + c0;  // key of column 0 in the tile
         const bool live = tl.live(i), mine = act && c0 < n2;
@@ -465,12 +473,71 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
         (void)warp_wait(&sh->drain[is_dq], 0, kDefaultWaitNs);
       }
     } else {
-      // ---------------------------------------------------------- dQ out (see tc_first_fwd.cu)
+      // ---------------------------------------------------------- delta, and dQ out (see tc_first_fwd.cu)
       const int g4 = warp & 3, hi = g4 >> 1, row0 = 32 * (g4 & 1);
       const uint32_t lane_base = tmem + ((uint32_t)(32 * g4) << 16);
       uint8_t* const st = stage + g4 * kStage;
       uint32_t npass = 0;
+      // delta of a pass's token while the pass before it runs: 16 rows a warp, two
+      // at a time, dout once more (out of L2, the producer loads it too)
+      Walk ahead(walk);
+      uint32_t nahead = 0;
+      auto delta_of_next = [&]() {
+        Pass pn;
+        if (!ahead.next(pn, nullptr)) return;
+        if (pn.active(rank)) {
+          const int t = pn.token(rank), units = p.dv / 8;
+          if (p.out && g4 == 0 && lane == 0) p.spoiled[t] = p.spoiled_keys[t] = 0;
+#pragma unroll 1
+          for (int r = 16 * g4; r < 16 * g4 + 16; r += 2) {
+            const int64_t th = (int64_t)t * kH + r;
+            float acc[2] = {0.f, 0.f};
+            if (p.out) {
+              uint4 x[2][2], y[2][2];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int e = lane + 32 * (k & 1);
+                x[k >> 1][k & 1] = y[k >> 1][k & 1] = make_uint4(0u, 0u, 0u, 0u);
+                if (e >= units) continue;
+                const int64_t at = (th + (k >> 1)) * p.dv + 8 * e;
+                x[k >> 1][k & 1] = __ldcs(reinterpret_cast<const uint4*>(p.out + at));
+                y[k >> 1][k & 1] = __ldg(reinterpret_cast<const uint4*>(p.dout + at));
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const __nv_bfloat162* const xp =
+                    reinterpret_cast<const __nv_bfloat162*>(&x[k >> 1][k & 1]);
+                const __nv_bfloat162* const yp =
+                    reinterpret_cast<const __nv_bfloat162*>(&y[k >> 1][k & 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                  const float2 u = __bfloat1622float2(xp[i]), v = __bfloat1622float2(yp[i]);
+                  acc[k >> 1] = fmaf(u.x, v.x, fmaf(u.y, v.y, acc[k >> 1]));
+                }
+              }
+              acc[0] = warp_sum(acc[0]);
+              acc[1] = warp_sum(acc[1]);
+            }
+            if (lane < 2) {
+              float d = lane ? acc[1] : acc[0];
+              if (p.out) {
+                p.delta[th + lane] = d;
+                p.dsink_part[th + lane] =
+                    p.sink ? -expf(__ldg(p.sink + r + lane) - __ldg(p.lse + th + lane)) * d : 0.f;
+              } else {
+                d = p.delta[th + lane];
+              }
+              sh->delta[nahead & 1][r + lane] = d;
+            }
+          }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->delfull[nahead & 1]);
+        ++nahead;
+      };
+      delta_of_next();
       while (ok && walk.next(ps, nullptr)) {
+        delta_of_next();
         if (!warp_wait(&sh->passdone, npass & 1, lim)) { ok = false; break; }
         tc_fence_after();
         if (ps.active(rank)) {
@@ -908,13 +975,10 @@ size_t tc_first_bwd_workspace(int total_tokens, int num_docs, int max_seqlen, in
   return n <= kMostBytes ? n : 0;
 }
 
-cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, const float* dsink_part,
-                                int* spoiled, int* spoiled_keys, void* ws, size_t ws_bytes,
-                                long long wait_limit, bool* taken, cudaStream_t s) {
-  *taken = false;
-  const Problem& p = b.p;
+namespace {
+Band band_of(const BwdArgs& b) {
+  const int longest = std::min(b.p.max_seqlen, b.p.total_tokens);
   Band band;
-  const int longest = std::min(p.max_seqlen, p.total_tokens);
   band.window = std::min(b.window, longest);
   // a window that holds every document leaves no first token outside
   band.first = band.window >= longest ? 0 : std::min(b.first, longest);
@@ -922,12 +986,28 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, const floa
   band.bw = (band.wp + 8 + 15) & ~15;
   band.fp = (band.first + 15) & ~15;
   band.stride = band_stride(band.window + band.first);
-  if (band.fp > pb::kKeys) return cudaSuccess;
-  const Sizes z = sizes_of(p.total_tokens, p.num_docs, band.window + band.first, band.window,
-                           band.fp, p.dk, p.dv);
-  if (!ws || 2 * z.band + z.wpart + z.fpart > ws_bytes) return cudaSuccess;
-  *taken = true;
-  uint8_t* w = static_cast<uint8_t*>(ws);
+  return band;
+}
+Sizes sizes_of(const BwdArgs& b, const Band& band) {
+  return sizes_of(b.p.total_tokens, b.p.num_docs, band.window + band.first, band.window, band.fp,
+                  b.p.dk, b.p.dv);
+}
+}  // namespace
+
+bool tc_first_bwd_takes(const BwdArgs& b) {
+  const Band band = band_of(b);
+  if (band.fp > pb::kKeys || !b.dkdv_ws) return false;
+  const Sizes z = sizes_of(b, band);
+  return 2 * z.band + z.wpart + z.fpart <= b.dkdv_bytes;
+}
+
+cudaError_t launch_tc_first_bwd(const BwdArgs& b, bool with_delta, float* delta, float* dsink_part,
+                                int* spoiled, int* spoiled_keys, long long wait_limit,
+                                cudaStream_t s) {
+  const Problem& p = b.p;
+  const Band band = band_of(b);
+  const Sizes z = sizes_of(b, band);
+  uint8_t* w = static_cast<uint8_t*>(b.dkdv_ws);
   __nv_bfloat16* const pband = reinterpret_cast<__nv_bfloat16*>(w);
   __nv_bfloat16* const sband = reinterpret_cast<__nv_bfloat16*>(w + z.band);
   CUtensorMap kmap, kmap16, vmap, vmap16, qmap, dmap, pw, pf, sw, sf;
@@ -957,19 +1037,31 @@ cudaError_t launch_tc_first_bwd(const BwdArgs& b, const float* delta, const floa
   a.dk = p.dk;
   a.scale = p.scale;
   a.scale_log2 = p.scale * kLog2e;
+  a.dv = p.dv;
   a.lse = b.lse;
+  a.sink = b.sink;
+  a.out = with_delta ? static_cast<const __nv_bfloat16*>(b.out) : nullptr;
+  a.dout = static_cast<const __nv_bfloat16*>(b.dout);
   a.delta = delta;
+  a.dsink_part = dsink_part;
   a.pband = pband;
   a.sband = sband;
   a.dq = static_cast<__nv_bfloat16*>(b.dq);
   a.spoiled = spoiled;
+  a.spoiled_keys = spoiled_keys;
   a.status = p.status;
   a.wait_ns = wait_limit > 0 ? wait_limit : kDefaultWaitNs;
   cudaError_t e = cudaFuncSetAttribute(pa::query_pass, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        (int)pa::kSmem);
   if (e != cudaSuccess) return e;
-  e = launch_after(pa::query_pass, pair_grid(T), pa::kThreads, pa::kSmem, s, kmap, kmap16, vmap,
-                   vmap16, qmap, dmap, a);
+  if (with_delta) {  // the call's first kernel
+    pa::query_pass<<<pair_grid(T), pa::kThreads, pa::kSmem, s>>>(kmap, kmap16, vmap, vmap16, qmap,
+                                                                dmap, a);
+    e = cudaGetLastError();
+  } else {
+    e = launch_after(pa::query_pass, pair_grid(T), pa::kThreads, pa::kSmem, s, kmap, kmap16, vmap,
+                     vmap16, qmap, dmap, a);
+  }
   if (e != cudaSuccess) return e;
   pb::Params k{};
   k.d = a.d;

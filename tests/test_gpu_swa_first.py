@@ -217,6 +217,39 @@ def test_malformed_documents_are_reported():
     assert bool((out[100:] == 7).all()) and not bool((out[:100] == 7).all())
 
 
+def test_backward_reports_malformed_documents():
+    """Rows in no document are reported; with a window that computes delta in the
+    query pass and with one that does not, the other rows keep their gradients."""
+    for W in (8, 400):
+        inp, dout = _inputs([400, 128], 64, 64, 512, BF16, 20)
+        out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 400, W, 2, inp.sink)
+        hs.poll_status()
+        cu = torch.tensor([0, 400, 500], device=DEV, dtype=torch.int32)
+        g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, cu, 400, W, 2, out, lse, dout, inp.sink)
+        with pytest.raises(hs.HSError) as e:
+            hs.poll_status()
+        assert e.value.status == hs.HS_ERR_INVALID_ARG
+        r = slice(0, 400)
+        ref = A.backward(inp.q[r], inp.k[r], inp.v[r], out[r], lse[r], dout[r], A.mask_of([0, 400], W, 2, DEV), None,
+                         64 ** -0.5, BF16)
+        A.check(g[0][r], *ref["dq"], "dq")
+
+
+@pytest.mark.parametrize("W", [20, 300])
+def test_backward_of_an_output_at_any_element(W):
+    """out one element past a 16-byte boundary."""
+    docs, F = [330, 41], 4
+    inp, dout = _inputs(docs, 64, 64, 512, BF16, 21)
+    args = (inp.cu_seqlens, 330, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    moved = torch.empty(out.numel() + 8, device=DEV, dtype=BF16)[1:out.numel() + 1].view(out.shape)
+    moved.copy_(out)
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, moved, lse, dout, inp.sink)
+    assert hs.last_path() == hs.HS_PATH_MMA
+    hs.poll_status()
+    _check_bwd(inp, W, F, inp.sink, out, lse, dout, g, BF16)
+
+
 def test_no_tokens():
     q = torch.zeros((0, 64, 576), device=DEV, dtype=BF16)
     k, v = q[:, 0], q[:, 0, :512]
