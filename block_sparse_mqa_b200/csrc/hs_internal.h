@@ -81,7 +81,7 @@ struct BwdArgs {
   int first = 0;       // swa only: first tokens of the document that stay visible
   bool with_first = false;       // the call is hs_swa_first_mqa_bwd (first may be 0)
   bool grad_like_input = false;  // dq, dkey, dval in p.dtype instead of fp32
-  void* workspace;     // simt_backward_workspace() bytes
+  void* workspace;     // simt_backward_workspace() bytes; with_first: 2 T flags behind them
   void* dkdv_ws;       // the tensor-core passes' workspace, or null
   size_t dkdv_bytes;
 };

@@ -268,6 +268,35 @@ def test_decode_shared_pages():
     _check_decode(q, rows, [x[:, :128] for x in rows], lens + [64], 0, 0, None, out, lse, BF16)
 
 
+@pytest.mark.parametrize("dk,H,path", [(64, 16, hs.HS_PATH_TCGEN05), (96, 2, hs.HS_PATH_SIMT)])
+def test_more_sequences_than_a_grid_dimension(dk, H, path):
+    """70001 sequences, each one of five over shared pages; then a token appended to
+    every one (pages of their own) and read back."""
+    lens, S, page = [1, 40, 0, 16, 130], 70001, 16
+    table, pool, kc, kv = _cache(lens, dk, page, 30)
+    of = torch.arange(S, device=DEV) % 5
+    q = torch.randn((5, H, dk), device=DEV).to(BF16)
+    out, lse = hs.hs_kv4_mqa_decode(q[of], kc, None, table[of].contiguous(), _i32(lens)[of].contiguous(), 130, page, 64)
+    assert hs.last_path() == path
+    hs.poll_status()
+    for s, n in enumerate(lens):
+        if n == 0:
+            assert not out[s::5].any() and bool((lse[s::5] == -torch.inf).all())
+            continue
+        mask = torch.ones((1, n), dtype=torch.bool, device=DEV)
+        ref, rl, bo, bl = A.forward(q[s:s + 1], kv[s], kv[s][:, :64], mask, None, dk ** -0.5, BF16)
+        A.check(out[s::5], ref.expand(out[s::5].shape), bo.expand(out[s::5].shape), "out")
+        A.check(lse[s::5], rl.expand(lse[s::5].shape), bl.expand(lse[s::5].shape), "lse")
+    x = torch.randn((S, dk), device=DEV).to(BF16)
+    cache, own = hs.kv4_cache(S, dk, page), torch.arange(S, device=DEV, dtype=torch.int32)[:, None]
+    cu, ones = torch.arange(S + 1, device=DEV, dtype=torch.int32), torch.ones(S, device=DEV, dtype=torch.int32)
+    hs.hs_kv4_append(x, None, cache, None, own, cu, ones, page)
+    got = hs.hs_kv4_read(cache, dk, own, cu, ones, page, S)
+    hs.poll_status()
+    some = slice(0, S, 997)
+    assert torch.equal(got[some].double().cpu(), torch.tensor(_values(x[some])))
+
+
 def test_decode_strided_and_unaligned_queries():
     lens, page = [90, 33], 32
     table, pool, kc, kv = _cache(lens, 192, page, 10)
