@@ -191,6 +191,32 @@ def test_deterministic_on_another_stream_and_in_a_graph(shape, dtype):
         assert torch.equal(a, b) and torch.equal(a, c) and torch.equal(d, e)
 
 
+def test_calls_side_by_side_on_two_streams():
+    """Forward and backward of two problems at once, narrow and wide windows, again
+    and again: bit for bit what each gives alone."""
+    cases = [(_inputs([300, 77, 1], 64, 192, 128, BF16, 22), 300, 20, 3),
+             (_inputs([410, 90], 64, 576, 512, BF16, 23), 410, 300, 5)]
+
+    def step(case):
+        (inp, dout), longest, W, F = case
+        args = (inp.cu_seqlens, longest, W, F)
+        out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+        return (out, lse) + tuple(hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink))
+
+    want = [step(c) for c in cases]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], [[], []]
+    for _ in range(6):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(step(cases[i]))
+    torch.cuda.synchronize()
+    hs.poll_status()
+    for w, runs in zip(want, got):
+        for g in runs:
+            assert all(torch.equal(a, b) for a, b in zip(w, g))
+
+
 def test_huge_logits_and_rows_without_weight():
     """Logits of +-3e4 (one key takes everything, others underflow) and a sink
     that takes everything."""
@@ -310,6 +336,20 @@ def test_other_passes_without_the_band():
     g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink, workspace=big)
     hs.poll_status()
     assert bool((big[want:] == 0xFF).all())
+    _check_bwd(inp, W, F, inp.sink, out, lse, dout, g, BF16)
+
+
+def test_a_workspace_full_of_nan():
+    """A window wide enough for delta in the query pass: nothing is read before it is written."""
+    docs, W, F = [500, 1, 90], 260, 6
+    inp, dout = _inputs(docs, 64, 192, 512, BF16, 24)
+    args = (inp.cu_seqlens, 500, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    want = hs.workspace_size(hs.HS_OP_SWA_FIRST_MQA_BWD, 591, 3, 500, 64, 192, 512, BF16, W + F)
+    ws = torch.full((want + 5000,), 0xFF, dtype=torch.uint8, device=DEV)
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink, workspace=ws)
+    hs.poll_status()
+    assert bool((ws[want:] == 0xFF).all())
     _check_bwd(inp, W, F, inp.sink, out, lse, dout, g, BF16)
 
 
