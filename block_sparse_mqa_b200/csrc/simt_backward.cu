@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kThreads) bwd_delta_kernel(const BwdParams a) 
 }
 
 // The same for aligned bf16 rows: every load of a row under way at once (114 ->
-// 90 us at 4096 tokens, 64 heads, Dv 512, where 0.54 GB have to be read).
+// 77 us at 4096 tokens, 64 heads, Dv 512, where 0.54 GB have to be read).
 __global__ void __launch_bounds__(kThreads) bwd_delta16_kernel(const BwdParams a) {
   const int64_t th = ((int64_t)blockIdx.x * kThreads + threadIdx.x) >> 5;
   const int lane = threadIdx.x & 31, dv = a.p.dv, units = dv / 8;
@@ -664,7 +664,7 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
     // (0 * NaN in a whole-tile product), is flagged and computed again.
     int* const flags = a.flags;
     int* const kflags = flags ? flags + (size_t)b.p.total_tokens : nullptr;
-    // the window's own passes, where their workspace was given
+    // the window's own passes, where their workspace was given,
     // and with delta in their query pass, if that has enough to do beside it (4096
     // tokens: Dk 576 / Dv 512 window 192 702 -> 730 us, 256 808 -> 796, 512 1109 ->
     // 1058; Dk 192 / Dv 128 window 512 619 -> 694, 1024 1045 -> 1022)
