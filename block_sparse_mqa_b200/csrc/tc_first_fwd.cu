@@ -83,7 +83,12 @@ struct Params {
 struct Shared {
   uint64_t kfull[kKSlots], kempty[kKSlots], vfull[kVSlots], vempty[kVSlots];
   uint64_t qfull[kMaxQC], qempty[kMaxQC];
-  uint64_t sfull[2], sempty[2], pfull, pvdone, oempty, drain[2], rv, stat;
+  uint64_t sfull[2], sempty[2], pfull, pvdone, oempty, drain[2], rv;
+  // A pass's sums are there, by pass parity: the softmax warps may be through the next
+  // pass before an epilogue warp looks, and one barrier, two phases on, would look as if
+  // the first had not come.  Two passes on is impossible: PV of pass n + 1 waits for
+  // oempty of pass n, and pass n + 2 for that PV.
+  uint64_t stat[2];
   float red[2][4][kH];
   float inv[2][kH];  // by pass parity
   uint32_t tmem_base;
@@ -134,7 +139,8 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     mbar_init(&sh->pvdone, 1);
     mbar_init(&sh->oempty, 8);  // 4 epilogue warps of each CTA
     mbar_init(&sh->rv, 8);
-    mbar_init(&sh->stat, 8);
+    mbar_init(&sh->stat[0], 8);
+    mbar_init(&sh->stat[1], 8);
     fence_barrier_init();
   }
   if (warp == kQkWarp) tmem_alloc_pair(&sh->tmem_base, 512);
@@ -304,9 +310,9 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
               den == 0.f ? -INFINITY : (Ms + fast_log2(den)) * kLn2;
         }
       }
-      ++npass;
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->stat);
+      if (lane == 0) mbar_arrive(&sh->stat[npass & 1]);
+      ++npass;
     }
     if (!ok && lane == 0) record_status(p.status, HS_ERR_TIMEOUT);
   } else {
@@ -478,7 +484,8 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       uint32_t npass = 0, npv = 0;
       while (ok && walk.next(ps, nullptr)) {
         npv += ps.ntile;
-        if (!warp_wait(&sh->stat, npass & 1, lim) || !warp_wait(&sh->pvdone, (npv - 1) & 1, lim)) {
+        if (!warp_wait(&sh->stat[npass & 1], (npass >> 1) & 1, lim) ||
+            !warp_wait(&sh->pvdone, (npv - 1) & 1, lim)) {
           ok = false;
           break;
         }

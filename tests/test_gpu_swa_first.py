@@ -431,6 +431,44 @@ def test_far_tokens_pass_32_bit_offsets():
         A.check(grads[i][rows], *(x[F + W:] for x in ref[name]), name)
 
 
+def _check_fwd_by_documents(inp, W, F, out, lse, most):
+    """Every row, `most` rows and the keys they may see at a time: documents are
+    joined while they fit, longer ones are cut into pieces of rows."""
+    cu, scale = inp.cu_seqlens.tolist(), inp.q.shape[2] ** -0.5
+    pieces, bos = [], 0  # (first key, first row, end, documents)
+    for d in range(1, len(cu)):
+        if d + 1 < len(cu) and cu[d + 1] - cu[bos] <= most:
+            continue
+        pieces += [(cu[bos], r, min(r + most, cu[d]), cu[bos:d + 1]) for r in range(cu[bos], cu[d], most)]
+        bos = d
+    for key0, r0, r1, ends in pieces:
+        rows = slice(r0, r1)
+        if len(ends) > 2:
+            keys = torch.arange(r0, r1, device=DEV)
+            mask = A.mask_of([e - key0 for e in ends], W, F, DEV)
+        else:  # the first tokens and what the rows' windows reach
+            keys = torch.cat([torch.arange(key0, min(key0 + F, r0), device=DEV),
+                              torch.arange(max(min(key0 + F, r0), r0 - W + 1), r1, device=DEV)])
+            t = torch.arange(r0, r1, device=DEV)[:, None]
+            mask = (keys <= t) & ((keys > t - W) | (keys < key0 + F))
+        ref, rlse, bo, bl = A.forward(inp.q[rows], inp.k[keys], inp.v[keys], mask, inp.sink, scale, BF16)
+        A.check(out[rows], ref, bo, "out")
+        A.check(lse[rows], rlse, bl, "lse")
+
+
+@pytest.mark.parametrize("docs", [[1, 2, 3, 1, 1] * 1500, [2] * 6000, [1] * 5000])
+def test_thousands_of_short_documents(docs):
+    """Passes of one tile, many for a pair, where finding the documents takes as long
+    as the pass: no role may run away from the others."""
+    W, F = 2, 1
+    inp, _ = _inputs(docs, 64, 64, 64, BF16, 25)
+    for _ in range(5):
+        out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 3, W, F, inp.sink)
+        assert hs.last_path() == hs.HS_PATH_TCGEN05
+        hs.poll_status()
+    _check_fwd_by_documents(inp, W, F, out, lse, 400)
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
