@@ -89,6 +89,10 @@ struct Shared {
   // the first had not come.  Two passes on is impossible: PV of pass n + 1 waits for
   // oempty of pass n, and pass n + 2 for that PV.
   uint64_t stat[2];
+  // What a row's four threads exchange, maxima and a pass's sums in turn.  An
+  // exchange writes one half, meets and reads it; the next one, of whichever pass,
+  // takes the other half, so a half is written again only after a meeting that
+  // every reader of it reached.
   float red[2][4][kH];
   float inv[2][kH];  // by pass parity
   uint32_t tmem_base;
@@ -165,7 +169,7 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
     const int row = 32 * (g4 & 1) + lane;
     const uint32_t lane_base = tmem + ((uint32_t)(32 * g4) << 16);
     const float sl2 = p.scale_log2;
-    uint32_t sidx = 0, npv = 0, rvph = 0, npass = 0;
+    uint32_t sidx = 0, npv = 0, rvph = 0, npass = 0;  // rvph: parity of the exchange, for red too
     auto meet = [&]() -> bool {  // the 8 warps of this CTA
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->rv);
@@ -232,10 +236,10 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
             mx = fmaxf(fmaxf(mx, fmaxf(m4[0], m4[1])), fmaxf(m4[2], m4[3]));
           }
           mx *= sl2;
-          sh->red[i & 1][part][row] = mx;
+          float(*const red)[kH] = sh->red[rvph];
+          red[part][row] = mx;
           if (!meet()) { ok = false; break; }
-          const float mt = fmaxf(fmaxf(sh->red[i & 1][0][row], sh->red[i & 1][1][row]),
-                                 fmaxf(sh->red[i & 1][2][row], sh->red[i & 1][3][row]));
+          const float mt = fmaxf(fmaxf(red[0][row], red[1][row]), fmaxf(red[2][row], red[3][row]));
           const float mn = mt > m + kRescaleLog2 ? mt : m;  // m = -inf: any logit raises it
           const float alpha = mn == m ? 1.f : fast_exp2(m - mn);
           m = mn;
@@ -295,12 +299,11 @@ tc_first_fwd_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_const
       if (!ok) break;
       // ---- the row's sum over its four threads and the sink, for the epilogue
       if (act) {
-        const int rb = ps.ntile & 1;
-        sh->red[rb][part][row] = l;
+        float(*const red)[kH] = sh->red[rvph];
+        red[part][row] = l;
         if (!meet()) { ok = false; break; }
         if (part == 0) {
-          const float lt = (sh->red[rb][0][row] + sh->red[rb][1][row]) +
-                           (sh->red[rb][2][row] + sh->red[rb][3][row]);
+          const float lt = (red[0][row] + red[1][row]) + (red[2][row] + red[3][row]);
           const float sk = p.sink ? __ldg(p.sink + row) * kLog2e : -INFINITY;
           const float M = fmaxf(m, sk), Ms = M == -INFINITY ? 0.f : M;
           const float em = m == -INFINITY ? 0.f : fast_exp2(m - Ms);

@@ -469,6 +469,21 @@ def test_thousands_of_short_documents(docs):
     _check_fwd_by_documents(inp, W, F, out, lse, 400)
 
 
+@pytest.mark.parametrize("docs,W,F", [([4096], 300, 4), ([4096], 1000, 8), ([2500, 1, 1500], 256, 0), ([3001], 512, 200)])
+def test_many_passes_of_several_tiles(docs, W, F):
+    """Two, three and four tiles of 256 keys a pass, many passes for a pair: a row's sum
+    is read while the next pass of its CTA may have begun.  Every row, again and again."""
+    inp, _ = _inputs(docs, 64, 64, 64, BF16, 26)
+    call = lambda: hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, inp.max_seqlen, W, F, inp.sink)
+    out, lse = call()
+    assert hs.last_path() == hs.HS_PATH_TCGEN05
+    hs.poll_status()
+    _check_fwd_by_documents(inp, W, F, out, lse, 256)
+    for _ in range(20):
+        o, l = call()
+        assert torch.equal(o, out) and torch.equal(l, lse)
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
