@@ -198,8 +198,9 @@ __device__ __forceinline__ void attend_row(const AttnArgs& a, int t, int h, floa
     if (tid < cnt) s = p.scale * dot_row<T>(qs, kb + (int64_t)(lo + tid) * p.k_row_stride, Dk);
     const float bmax = block_reduce_max(s, red);
     const float mn = fmaxf(m, bmax);
-    const float alpha = expf(m - mn);  // 0 on the first segment
-    const float pv = (tid < cnt) ? expf(s - mn) : 0.f;
+    const float ms = mn == -INFINITY ? 0.f : mn;  // every logit so far is -inf
+    const float alpha = expf(m - ms);  // 0 on the first segment
+    const float pv = (tid < cnt) ? expf(s - ms) : 0.f;
     pbuf[tid] = pv;
     const float psum = block_reduce_sum(pv, red);  // also orders the pbuf writes
     l = l * alpha + psum;

@@ -484,6 +484,54 @@ def test_many_passes_of_several_tiles(docs, W, F):
         assert torch.equal(o, out) and torch.equal(l, lse)
 
 
+@pytest.mark.parametrize("H,dk,dv,dtype,simt", [(4, 64, 48, F32, False), (4, 64, 48, BF16, False),
+                                                (64, 192, 128, BF16, False), (64, 192, 128, BF16, True)])
+@pytest.mark.parametrize("low", [float("-inf"), -3e38])
+def test_first_keys_of_weight_zero(H, dk, dv, dtype, simt, low):
+    """A key whose logit is -inf (held, or past fp32) takes no weight, though it is the
+    first one alone that a running maximum meets."""
+    docs, W, F = [150, 1, 330], 20, 1
+    inp, _ = _inputs(docs, H, dk, dv, dtype, 27)
+    cu = inp.cu_seqlens.tolist()
+    inp.q[:, :, 0] = 1000.0
+    inp.k[:, 0] = 0.0
+    inp.k[cu[:-1], 0] = low
+    hs.set_force_simt(simt)
+    try:
+        out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, 330, W, F, inp.sink)
+    finally:
+        hs.set_force_simt(False)
+    hs.poll_status()
+    mask = A.mask_of(cu, W, F, DEV)
+    mask[:, cu[:-1]] = False
+    ref, rlse, bo, bl = A.forward(inp.q, inp.k, inp.v, mask, inp.sink, dk ** -0.5, dtype)
+    A.check(out, ref, bo, "out")
+    A.check(lse, rlse, bl, "lse")
+
+
+def test_a_first_segment_of_weight_zero():
+    """The same for the first 128 keys of a window and for a first selected block."""
+    T, H, dk, dv, W = 300, 4, 64, 48, 260
+    inp, _ = _inputs([T], H, dk, dv, F32, 28)
+    inp.q[:, :, 0] = 1000.0
+    inp.k[:, 0] = 0.0
+    inp.k[:200, 0] = float("-inf")
+    rows, t = slice(250, T), torch.arange(250, T, device=DEV)[:, None]
+    j = torch.arange(T, device=DEV)
+    out, lse = hs.hs_swa_mqa_fwd(inp.q, inp.k, inp.v, inp.cu_seqlens, T, W, inp.sink)
+    hs.poll_status()
+    ref, rlse, bo, bl = A.forward(inp.q[rows], inp.k, inp.v, (j <= t) & (j >= 200), inp.sink, dk ** -0.5, F32)
+    A.check(out[rows], ref, bo, "out")
+    A.check(lse[rows], rlse, bl, "lse")
+    idx = torch.stack([torch.zeros_like(j), j // 16], 1).int()
+    idx[:16, 1] = -1
+    out, lse = hs.hs_sparse_mqa_fwd(inp.q, inp.k, inp.v, idx, inp.cu_seqlens, T, 16, inp.sink)
+    hs.poll_status()
+    ref, rlse, bo, bl = A.forward(inp.q[rows], inp.k, inp.v, (j <= t) & (j // 16 == t // 16), inp.sink, dk ** -0.5, F32)
+    A.check(out[rows], ref, bo, "out")
+    A.check(lse[rows], rlse, bl, "lse")
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
