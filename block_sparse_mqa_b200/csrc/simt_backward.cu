@@ -665,11 +665,15 @@ cudaError_t launch_simt_backward(const BwdArgs& b, bool sparse, bool allow_mma, 
     int* const flags = a.flags;
     int* const kflags = flags ? flags + (size_t)b.p.total_tokens : nullptr;
     // the window's own passes, where their workspace was given,
-    // and with delta in their query pass, if that has enough to do beside it (4096
-    // tokens: Dk 576 / Dv 512 window 192 702 -> 730 us, 256 808 -> 796, 512 1109 ->
-    // 1058; Dk 192 / Dv 128 window 512 619 -> 694, 1024 1045 -> 1022)
+    // and with delta in their query pass, if that has enough to do beside it (one
+    // document of 4096 tokens: Dk 576 / Dv 512 window 192 702 -> 730 us, 256 808 ->
+    // 796, 512 1109 -> 1058; Dk 192 / Dv 128 window 512 619 -> 694, 1024 1045 ->
+    // 1022): the keys are those a token can attend, none past its document (documents
+    // of 64 to 200 tokens, window 512, Dk 576 / Dv 512: 543-681 -> 490-630 us)
     const bool own = mma && b.with_first && tc_first_bwd_takes(b);
-    const int64_t keys = (int64_t)b.window + b.first;
+    const int64_t longest = b.p.max_seqlen < b.p.total_tokens ? b.p.max_seqlen : b.p.total_tokens;
+    const int64_t nominal = (int64_t)b.window + b.first;
+    const int64_t keys = nominal < longest ? nominal : longest;
     const bool with_delta = own && al16(b.out) && keys * b.p.dv >= 120000;
     cudaError_t e = cudaSuccess;
     if (own) a.dsink = nullptr;  // a part of their reduction

@@ -1,6 +1,8 @@
 """hs_swa_first_mqa_fwd / _bwd against a dense-mask form in float64
 (tests/attn64.py, which also gives the error bounds), and against the oracle."""
 
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -530,6 +532,35 @@ def test_a_first_segment_of_weight_zero():
     ref, rlse, bo, bl = A.forward(inp.q[rows], inp.k, inp.v, (j <= t) & (j // 16 == t // 16), inp.sink, dk ** -0.5, F32)
     A.check(out[rows], ref, bo, "out")
     A.check(lse[rows], rlse, bl, "lse")
+
+
+def _graph_nodes(call):
+    """Kernels that call() launches."""
+    call()
+    graph = torch.cuda.CUDAGraph(keep_graph=True)
+    with torch.cuda.graph(graph):
+        call()
+    n = ctypes.c_size_t()
+    assert ctypes.CDLL("libcuda.so.1").cuGraphGetNodes(ctypes.c_void_p(graph.raw_cuda_graph()), None, ctypes.byref(n)) == 0
+    return n.value
+
+
+def test_a_window_past_the_documents_takes_the_same_kernels():
+    """Where delta is computed goes by the keys that a token can attend, not by the
+    window's number: packed short documents with a window that holds each of them."""
+    docs, F = [60, 33, 64, 7] * 6, 4
+    inp, dout = _inputs(docs, 64, 64, 512, BF16, 29)
+    nodes, grads = [], []
+    for W in (64, 512, 2 ** 31 - 1):
+        args = (inp.cu_seqlens, 64, W, F)
+        out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+        call = lambda: hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink)
+        nodes.append(_graph_nodes(call))
+        grads.append(call())
+    hs.poll_status()
+    assert nodes[0] == nodes[1] == nodes[2]
+    for g in grads[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(g, grads[0]))
 
 
 def test_without_tensor_cores():
