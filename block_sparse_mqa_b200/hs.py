@@ -561,6 +561,13 @@ def _new_or(t, name, shape, dtype, like):
     return t
 
 
+def _space(workspace):
+    """Address and bytes of a workspace, which has to be one piece of memory."""
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
 def _sink_ok(sink, H):
     if sink is not None:
         _out("sink", sink, (H,), torch.float32)
@@ -630,7 +637,7 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
           _addr(v), _row_stride(v), _addr(cu_seqlens), nd, T, int(max_seqlen), H, Dk, Dv,
           _dtype_code(q), float(softmax_scale), int(window), int(num_first), _addr(sink),
           _addr(out), _addr(lse), _addr(dout), _addr(grads[0]), _addr(grads[1]), _addr(grads[2]),
-          _addr(grads[3]), _addr(workspace), workspace.numel() * workspace.element_size())
+          _addr(grads[3]), *_space(workspace))
     return grads
 
 
@@ -747,7 +754,7 @@ def hs_kv4_mqa_decode(q, k_cache, v_cache, block_table, seq_lens, max_seqlen: in
     _call(lib().hs_kv4_mqa_decode, index, _addr(q), qrs, qhs, _addr(k_cache), _addr(v_cache),
           *table, _addr(seq_lens), S, int(max_seqlen), H, Dk, int(dv), _dtype_code(q),
           float(softmax_scale), int(window), int(num_first), _addr(sink), _addr(o), _addr(l),
-          _addr(workspace), workspace.numel() * workspace.element_size())
+          *_space(workspace))
     return o, l
 
 

@@ -127,3 +127,43 @@ def test_binding_refuses_cpu_tensors():
     with pytest.raises(ValueError):
         hs.hs_kv4_mqa_decode(q, c, None, torch.zeros((4, 1), dtype=torch.int32), torch.zeros(4, dtype=torch.int32), 4,
                              16, 32)
+
+
+class _Launch(Exception):
+    pass
+
+
+@pytest.fixture
+def recorded(monkeypatch):
+    """The binding on CPU tensors up to the library call, whose arguments it raises."""
+    def call(fn, index, *args):
+        raise _Launch(args)
+
+    monkeypatch.setattr(hs, "_same_device", lambda *ts: 0)
+    monkeypatch.setattr(hs, "_call", call)
+
+
+def _backward(workspace):
+    q, k, lse = torch.zeros(8, 4, 32), torch.zeros(8, 32), torch.zeros(8, 4)
+    cu = torch.tensor([0, 8], dtype=torch.int32)
+    return hs.hs_swa_first_mqa_bwd(q, k, k, cu, 8, 4, 1, q, lse, q, workspace=workspace)
+
+
+def _decode(workspace, maxlen=40, window=0, first=0):
+    cache, table = torch.zeros((4, 16 * 20), dtype=torch.uint8), torch.zeros((2, 3), dtype=torch.int32)
+    return hs.hs_kv4_mqa_decode(torch.zeros(2, 4, 32), cache, None, table, torch.zeros(2, dtype=torch.int32), maxlen, 16,
+                                32, window, first, workspace=workspace)
+
+
+@pytest.mark.parametrize("call", [_backward, _decode])
+def test_a_workspace_that_is_not_one_piece(recorded, call):
+    """Its number of elements says nothing about the bytes behind its first one."""
+    size = 1 << 20
+    for ws in (torch.zeros(1, dtype=torch.uint8).expand(size), torch.zeros(2 * size, dtype=torch.uint8)[::2],
+               torch.zeros(8, 4).expand(1000, 8, 4)):
+        with pytest.raises(ValueError, match="workspace"):
+            call(ws)
+    for ws, n in ((torch.zeros(size, dtype=torch.uint8), size), (torch.zeros(1000, 8), 32000)):
+        with pytest.raises(_Launch) as e:
+            call(ws)
+        assert e.value.args[0][-2:] == (ws.data_ptr(), n)
