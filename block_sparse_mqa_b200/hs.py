@@ -493,6 +493,12 @@ def _addr(t):
     return None if t is None else t.data_ptr()
 
 
+def _c_int(x):
+    """A bound as a C int.  ctypes would keep the lowest 32 bits; past every length
+    there can be, the largest int means the same."""
+    return max(-2 ** 31, min(int(x), 2 ** 31 - 1))
+
+
 def _same_device(first, *rest):
     """Device index of the tensors (None is skipped)."""
     if not first.is_cuda:
@@ -598,8 +604,9 @@ def hs_swa_first_mqa_fwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
     if T == 0:
         return o, l
     _call(lib().hs_swa_first_mqa_fwd, index, _addr(q), qrs, qhs, _addr(k), _row_stride(k),
-          _addr(v), _row_stride(v), _addr(cu_seqlens), cu_seqlens.numel() - 1, T, int(max_seqlen),
-          H, Dk, Dv, _dtype_code(q), float(softmax_scale), int(window), int(num_first),
+          _addr(v), _row_stride(v), _addr(cu_seqlens), cu_seqlens.numel() - 1, T,
+          _c_int(max_seqlen), H, Dk, Dv, _dtype_code(q), float(softmax_scale), _c_int(window),
+          _c_int(num_first),
           _addr(sink), _addr(o), _addr(l))
     return o, l
 
@@ -623,19 +630,20 @@ def hs_swa_first_mqa_bwd(q, k, v, cu_seqlens, max_seqlen: int, window: int, num_
         _out(name, g, shape, q.dtype)
     _sink_ok(grads[3], H)
     nd = cu_seqlens.numel() - 1
+    max_seqlen, window, num_first = _c_int(max_seqlen), _c_int(window), _c_int(num_first)
     if T == 0:
         if grads[3] is not None:
             grads[3].zero_()
         return grads
     if workspace is None:
-        most = min(int(max_seqlen), T)
-        span = min(int(window), most) + min(int(num_first), most)
-        workspace = torch.empty(_sizes(HS_OP_SWA_FIRST_MQA_BWD, T, nd, int(max_seqlen), H, Dk, Dv,
+        most = min(max_seqlen, T)
+        span = min(window, most) + min(num_first, most)
+        workspace = torch.empty(_sizes(HS_OP_SWA_FIRST_MQA_BWD, T, nd, max_seqlen, H, Dk, Dv,
                                        q.dtype, span),
                                 device=q.device, dtype=torch.uint8)
     _call(lib().hs_swa_first_mqa_bwd, index, _addr(q), qrs, qhs, _addr(k), _row_stride(k),
-          _addr(v), _row_stride(v), _addr(cu_seqlens), nd, T, int(max_seqlen), H, Dk, Dv,
-          _dtype_code(q), float(softmax_scale), int(window), int(num_first), _addr(sink),
+          _addr(v), _row_stride(v), _addr(cu_seqlens), nd, T, max_seqlen, H, Dk, Dv,
+          _dtype_code(q), float(softmax_scale), window, num_first, _addr(sink),
           _addr(out), _addr(lse), _addr(dout), _addr(grads[0]), _addr(grads[1]), _addr(grads[2]),
           _addr(grads[3]), *_space(workspace))
     return grads
@@ -747,13 +755,14 @@ def hs_kv4_mqa_decode(q, k_cache, v_cache, block_table, seq_lens, max_seqlen: in
     l = _new_or(lse, "lse", (S, H), torch.float32, q)
     if S == 0:
         return o, l
+    max_seqlen = _c_int(max_seqlen)
     if workspace is None:
-        workspace = torch.empty(_sizes(HS_OP_KV4_MQA_DECODE, S, S, int(max_seqlen), H, Dk, int(dv),
+        workspace = torch.empty(_sizes(HS_OP_KV4_MQA_DECODE, S, S, max_seqlen, H, Dk, int(dv),
                                        q.dtype, int(page_size)),
                                 device=q.device, dtype=torch.uint8)
     _call(lib().hs_kv4_mqa_decode, index, _addr(q), qrs, qhs, _addr(k_cache), _addr(v_cache),
-          *table, _addr(seq_lens), S, int(max_seqlen), H, Dk, int(dv), _dtype_code(q),
-          float(softmax_scale), int(window), int(num_first), _addr(sink), _addr(o), _addr(l),
+          *table, _addr(seq_lens), S, max_seqlen, H, Dk, int(dv), _dtype_code(q),
+          float(softmax_scale), _c_int(window), _c_int(num_first), _addr(sink), _addr(o), _addr(l),
           *_space(workspace))
     return o, l
 

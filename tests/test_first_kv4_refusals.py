@@ -167,3 +167,24 @@ def test_a_workspace_that_is_not_one_piece(recorded, call):
         with pytest.raises(_Launch) as e:
             call(ws)
         assert e.value.args[0][-2:] == (ws.data_ptr(), n)
+
+
+@pytest.mark.parametrize("far", [2 ** 31, 2 ** 32, 2 ** 32 + 5, 2 ** 63 - 1])
+def test_sizes_past_32_bits_are_not_cut(recorded, far):
+    """A window, first tokens or bound past a C int mean what the largest int means."""
+    top = 2 ** 31 - 1
+    q, k, lse = torch.zeros(8, 4, 32), torch.zeros(8, 32), torch.zeros(8, 4)
+    cu = torch.tensor([0, 8], dtype=torch.int32)
+    with pytest.raises(_Launch) as e:
+        hs.hs_swa_first_mqa_fwd(q, k, k, cu, far, far, far)
+    with pytest.raises(_Launch) as f:
+        hs.hs_swa_first_mqa_bwd(q, k, k, cu, far, far, far, q, lse, q)
+    with pytest.raises(_Launch) as g:
+        _decode(torch.zeros(1 << 20), far, far, far)
+    for args, n in ((e.value.args[0], 3), (f.value.args[0], 3), (g.value.args[0], 3)):
+        assert sum(a == top for a in args if isinstance(a, int)) == n
+        assert not any(a == far for a in args if isinstance(a, int))
+    for low in (-1, -2 ** 31 - 1, -2 ** 40):  # refused by the library, whatever bits they end in
+        with pytest.raises(_Launch) as e:
+            hs.hs_swa_first_mqa_fwd(q, k, k, cu, 8, low, 1)
+        assert any(isinstance(a, int) and -2 ** 31 <= a < 0 for a in e.value.args[0])
