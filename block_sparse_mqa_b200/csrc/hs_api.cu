@@ -891,7 +891,9 @@ hs_status hs_kv4_mqa_decode(const void* q, int64_t q_row_stride, int64_t q_head_
   a.ps_log2 = log2_of(page_size);
   a.seq_lens = seq_lens;
   a.num_seqs = num_seqs;
-  a.max_seqlen = max_seqlen;
+  // a longer one counts as out of range: the kernels add a tile's or a split's size
+  // to key counts in 32 bits
+  a.max_seqlen = std::min(max_seqlen, INT32_MAX - 4095);
   a.num_heads = num_heads;
   a.dk = dk;
   a.dv = dv;

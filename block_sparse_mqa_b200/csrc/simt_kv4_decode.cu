@@ -25,7 +25,7 @@ constexpr int kMaxCols = 4;  // value columns per thread (dv <= 1024)
 int num_splits(int num_seqs, int num_heads, int max_keys) {
   const int64_t ctas = (int64_t)num_seqs * ((num_heads + kHB - 1) / kHB);
   int64_t n = (2 * 148 + ctas - 1) / ctas;
-  const int64_t most = (max_keys + 63) / 64;
+  const int64_t most = ((int64_t)max_keys + 63) / 64;
   if (n > most) n = most;
   return n < 1 ? 1 : n > 256 ? 256 : (int)n;
 }

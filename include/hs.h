@@ -524,8 +524,8 @@ hs_status hs_kv4_read(const void* cache, int width, const int32_t* block_table,
  *   q           [num_seqs, H, Dk] of `dtype`
  *   k_cache     plane of width Dk; v_cache plane of width Dv with the same
  *               block table, or NULL: the first Dv <= Dk columns of the keys
- *   max_seqlen  host-side bound of seq_lens (a longer one is
- *               HS_ERR_INVALID_ARG in the device status, and is treated as 0);
+ *   max_seqlen  host-side bound of seq_lens (a longer one, or one past 2^31 - 4096,
+ *               is HS_ERR_INVALID_ARG in the device status, and is treated as 0);
  *               num_seqs * ceil(keys attended / 128) at this bound must fit 31 bits
  *   out         [num_seqs, H, Dv] of `dtype`, contiguous; lse [num_seqs, H] fp32
  *   workspace   hs_workspace_size(HS_OP_KV4_MQA_DECODE, num_seqs, num_seqs,

@@ -188,3 +188,10 @@ def test_sizes_past_32_bits_are_not_cut(recorded, far):
         with pytest.raises(_Launch) as e:
             hs.hs_swa_first_mqa_fwd(q, k, k, cu, 8, low, 1)
         assert any(isinstance(a, int) and -2 ** 31 <= a < 0 for a in e.value.args[0])
+
+
+@pytest.mark.parametrize("dk,dv,dt", [(576, 512, torch.float32), (96, 32, torch.bfloat16)])
+def test_decode_workspace_of_the_largest_bound(dk, dv, dt):
+    """A bound of the largest int asks for what one a little below it does."""
+    size = lambda maxlen: hs.workspace_size(hs.HS_OP_KV4_MQA_DECODE, 2, 2, maxlen, 64, dk, dv, dt, 16)
+    assert size(2 ** 31 - 1) == size(2 ** 31 - 5000) > size(64)

@@ -344,6 +344,22 @@ def test_decode_bad_lengths_and_pages_are_reported():
             _check_decode(q[1:], kv[1:], kv[1:], [20], 0, 0, None, out[1:], lse[1:], BF16)
 
 
+@pytest.mark.parametrize("dk,path", [(64, hs.HS_PATH_TCGEN05), (96, hs.HS_PATH_SIMT)])
+def test_decode_lengths_at_the_end_of_int(dk, path):
+    """The largest int as bound, and as a length: reported, and no key of it is looked for."""
+    page, lens = 16, [40, 2 ** 31 - 1, 20, 2 ** 31 - 4095]
+    table, pool, kc, kv = _cache([40, 1, 20, 1], dk, page, 31)
+    q = torch.randn((4, 64, dk), device=DEV).to(BF16)
+    for window, first in ((0, 0), (10, 2)):
+        out, lse = hs.hs_kv4_mqa_decode(q, kc, None, table, _i32(lens), 2 ** 31 - 1, page, 64, window, first)
+        assert hs.last_path() == path
+        with pytest.raises(hs.HSError) as e:
+            hs.poll_status()
+        assert e.value.status == hs.HS_ERR_INVALID_ARG
+        n, val = [40, 0, 20, 0], [kv[0], kv[0][:0], kv[2], kv[0][:0]]
+        _check_decode(q, val, [x[:, :64] for x in val], n, window, first, None, out, lse, BF16)
+
+
 def test_decode_streams_and_graphs_with_growing_sequences():
     """A captured step (append one token to each sequence, attend) replayed while
     the lengths move on the device; two graphs and an eager call, each its own workspace."""
