@@ -699,21 +699,22 @@ hs_status hs_swa_first_mqa_bwd(const void* q, int64_t q_row_stride, int64_t q_he
                                void* workspace, size_t workspace_bytes, hs_stream_t stream) {
   hs_status r = check_window_first(window, num_first, total_tokens);
   if (r != HS_OK) return r;
-  // no tokens: the sink's gradient is the one output that still has elements
-  if (total_tokens == 0 && sink && dsink && num_heads >= 1 && num_heads <= kMaxHeads) {
-    const cudaError_t e = cudaMemsetAsync(dsink, 0, sizeof(float) * num_heads, stream);
-    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
-  }
   hs::BwdArgs a{};
   a.block_size = 64;
   a.window = window;
   a.first = num_first;
   a.with_first = true;
   a.grad_like_input = true;
-  return backward_common(a, false, q, q_row_stride, q_head_stride, k, k_row_stride, v,
-                         v_row_stride, cu_seqlens, num_docs, total_tokens, max_seqlen, num_heads,
-                         dk, dv, dtype, softmax_scale, sink, out, lse, dout, dq, dkey, dval,
-                         dsink, workspace, workspace_bytes, stream);
+  r = backward_common(a, false, q, q_row_stride, q_head_stride, k, k_row_stride, v, v_row_stride,
+                      cu_seqlens, num_docs, total_tokens, max_seqlen, num_heads, dk, dv, dtype,
+                      softmax_scale, sink, out, lse, dout, dq, dkey, dval, dsink, workspace,
+                      workspace_bytes, stream);
+  // no tokens: the sink's gradient is the one output that still has elements
+  if (r == HS_OK && total_tokens == 0 && sink && dsink) {
+    const cudaError_t e = cudaMemsetAsync(dsink, 0, sizeof(float) * num_heads, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "cudaMemsetAsync");
+  }
+  return r;
 }
 
 // ------------------------------------------------------------ 4-bit cache

@@ -195,3 +195,10 @@ def test_decode_workspace_of_the_largest_bound(dk, dv, dt):
     """A bound of the largest int asks for what one a little below it does."""
     size = lambda maxlen: hs.workspace_size(hs.HS_OP_KV4_MQA_DECODE, 2, 2, maxlen, 64, dk, dv, dt, 16)
     assert size(2 ** 31 - 1) == size(2 ** 31 - 5000) > size(64)
+
+
+@pytest.mark.parametrize("kw,code", [(dict(dk=0), UNS), (dict(dt=7), UNS), (dict(window=0), INV), (dict(out=None), INV),
+                                     (dict(dq=None), INV), (dict(scale=float("nan")), INV), (dict(krs=5), INV)])
+def test_backward_of_no_tokens_refuses_first(kw, code):
+    """The sink's gradient is cleared only by a call whose arguments are right."""
+    assert _call("hs_swa_first_mqa_bwd", BWD, dict(T=0, nd=0, maxlen=0, sink=256, dsink=256, **kw)) == code
