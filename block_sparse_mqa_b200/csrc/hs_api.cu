@@ -875,7 +875,7 @@ hs_status hs_kv4_mqa_decode(const void* q, int64_t q_row_stride, int64_t q_head_
   if (num_seqs == 0) return HS_OK;
   const size_t need = hs_workspace_size(HS_OP_KV4_MQA_DECODE, num_seqs, num_seqs, max_seqlen,
                                         num_heads, dk, dv, dtype, page_size);
-  if (!workspace || workspace_bytes < need)
+  if (need > 0 && (!workspace || workspace_bytes < need))
     return fail(HS_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need,
                 workspace ? workspace_bytes : (size_t)0);
   if (!aligned16(workspace)) return fail(HS_ERR_INVALID_ARG, "workspace is not 16-byte aligned");

@@ -6,7 +6,9 @@
 // One CTA per (split of the key list, 4 heads, sequence) walks its keys in
 // tiles of 32 rows staged in shared memory as fp32, with a running maximum and
 // sum per head; a second kernel joins the splits in their order and adds the
-// sink.  Every sum has a fixed order.
+// sink.  A lone split is finished by its CTA, without a workspace, so that many
+// sequences need none (partials of every sequence would take 9 GB for 70000 with
+// 64 heads, Dv 512).  Every sum has a fixed order.
 
 #include <math.h>
 
@@ -66,6 +68,12 @@ __device__ __forceinline__ int seq_len(const Kv4Decode& a, int b) {
     return 0;
   }
   return len;
+}
+
+// 1 / den and the lse, for a sum den of exponentials over exp(Ms).
+__device__ __forceinline__ float2 inv_and_lse(float den, float Ms) {
+  return make_float2(den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den),  // NaN stays NaN
+                     den == 0.f ? -INFINITY : Ms + logf(den));
 }
 
 template <typename T>
@@ -164,6 +172,16 @@ simt_kv4_decode_kernel(const Kv4Decode a, int nsplit, float* part_o, float2* par
     __syncthreads();
     for (int h = 0; h < hn; ++h) {
       const int64_t slot = ((int64_t)b * H + h0 + h) * nsplit + split;
+      // a lone split: what the join below would do with it, rounded alike
+      float w = 1.f, inv = 1.f;
+      if (nsplit == 1) {
+        const float sk = a.sink ? __ldg(a.sink + h0 + h) : -INFINITY;
+        const float M = fmaxf(sk, mrun[h]), Ms = M == -INFINITY ? 0.f : M;
+        w = expf(mrun[h] - Ms);
+        const float2 r = inv_and_lse(__fmul_rn(lrun[h], w) + expf(sk - Ms), Ms);
+        inv = r.x;
+        if (tid == 0) a.lse[slot] = r.y;
+      }
 #pragma unroll
       for (int c = 0; c < kMaxCols; ++c) {
         const int d = tid + c * kThreads;
@@ -172,10 +190,13 @@ simt_kv4_decode_kernel(const Kv4Decode a, int nsplit, float* part_o, float2* par
 #pragma unroll
           for (int hh = 0; hh < kHB; ++hh)
             if (hh == h) v = acc[hh][c];
-          part_o[slot * dv + d] = v;
+          if (nsplit == 1)
+            static_cast<T*>(a.out)[slot * dv + d] = from_f32<T>(__fmul_rn(v, w) * inv);
+          else
+            part_o[slot * dv + d] = v;
         }
       }
-      if (tid == 0) part_ml[slot] = make_float2(mrun[h], lrun[h]);
+      if (nsplit > 1 && tid == 0) part_ml[slot] = make_float2(mrun[h], lrun[h]);
     }
   }
 }
@@ -196,14 +217,14 @@ simt_kv4_join_kernel(const Kv4Decode a, int nsplit, const float* part_o, const f
     den += ml.y * expf(ml.x - Ms);
   }
   den += expf(sk - Ms);
-  const float inv = den > 0.f ? 1.f / den : (den == 0.f ? 0.f : den);  // NaN stays NaN
+  const float2 r = inv_and_lse(den, Ms);
   for (int d = threadIdx.x; d < a.dv; d += kThreads) {
     float o = 0.f;
     for (int i = 0; i < nsplit; ++i)
       o = fmaf(part_o[(bh * nsplit + i) * a.dv + d], expf(part_ml[bh * nsplit + i].x - Ms), o);
-    static_cast<T*>(a.out)[bh * a.dv + d] = from_f32<T>(o * inv);
+    static_cast<T*>(a.out)[bh * a.dv + d] = from_f32<T>(o * r.x);
   }
-  if (threadIdx.x == 0) a.lse[bh] = den == 0.f ? -INFINITY : Ms + logf(den);
+  if (threadIdx.x == 0) a.lse[bh] = r.y;
 }
 
 size_t smem_bytes(int dk, int dv) {
@@ -225,7 +246,7 @@ cudaError_t launch_typed(const Kv4Decode& a, cudaStream_t s) {
   const dim3 grid(nsplit, (a.num_heads + kHB - 1) / kHB, a.num_seqs < 65535 ? a.num_seqs : 65535);
   kern<<<grid, kThreads, bytes, s>>>(a, nsplit, po, ml);
   e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || nsplit == 1) return e;
   simt_kv4_join_kernel<T><<<(unsigned)((int64_t)a.num_seqs * a.num_heads), kThreads, 0, s>>>(
       a, nsplit, po, ml);
   return cudaGetLastError();
@@ -234,8 +255,9 @@ cudaError_t launch_typed(const Kv4Decode& a, cudaStream_t s) {
 }  // namespace
 
 size_t simt_kv4_decode_workspace(int num_seqs, int num_heads, int max_seqlen, int dv) {
-  return (size_t)num_seqs * num_heads * num_splits(num_seqs, num_heads, max_seqlen) *
-         (sizeof(float2) + (size_t)dv * sizeof(float));
+  const int nsplit = num_splits(num_seqs, num_heads, max_seqlen);
+  if (nsplit == 1) return 0;
+  return (size_t)num_seqs * num_heads * nsplit * (sizeof(float2) + (size_t)dv * sizeof(float));
 }
 
 cudaError_t launch_simt_kv4_decode(const Kv4Decode& a, cudaStream_t s) {

@@ -529,9 +529,9 @@ hs_status hs_kv4_read(const void* cache, int width, const int32_t* block_table,
  *               num_seqs * ceil(keys attended / 128) at this bound must fit 31 bits
  *   out         [num_seqs, H, Dv] of `dtype`, contiguous; lse [num_seqs, H] fp32
  *   workspace   hs_workspace_size(HS_OP_KV4_MQA_DECODE, num_seqs, num_seqs,
- *               max_seqlen, H, Dk, Dv, dtype, page_size) bytes, 16-byte
- *               aligned, contents on entry do not matter; calls that may
- *               overlap must not share one.
+ *               max_seqlen, H, Dk, Dv, dtype, page_size) bytes (0 = none, at most
+ *               about 40 MB and 4 a sequence), 16-byte aligned, contents on
+ *               entry do not matter; calls that may overlap must not share one.
  * Results are deterministic; how a sequence's keys are split over the GPU,
  * and so the last bits, depends on the whole batch's lengths.
  */

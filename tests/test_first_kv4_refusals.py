@@ -202,3 +202,14 @@ def test_decode_workspace_of_the_largest_bound(dk, dv, dt):
 def test_backward_of_no_tokens_refuses_first(kw, code):
     """The sink's gradient is cleared only by a call whose arguments are right."""
     assert _call("hs_swa_first_mqa_bwd", BWD, dict(T=0, nd=0, maxlen=0, sink=256, dsink=256, **kw)) == code
+
+
+@pytest.mark.parametrize("H,dk,dv,dt", [(64, 576, 512, torch.bfloat16), (128, 576, 512, torch.bfloat16),
+                                        (128, 1024, 1024, torch.float32), (1, 32, 32, torch.bfloat16)])
+def test_decode_workspace_does_not_grow_with_the_batch(H, dk, dv, dt):
+    """Partial results of as many pieces as fill the GPU, and 4 bytes a sequence."""
+    for S in (1, 7, 100, 2000, 70001):
+        for most in (1, 200, 10 ** 5):
+            need = hs.workspace_size(hs.HS_OP_KV4_MQA_DECODE, S, S, most, H, dk, dv, dt, 64)
+            assert need <= 148 * 2 * 64 * (8 + 4 * dv) + 4 * S + 16, (S, most, need)
+    assert _call("hs_kv4_mqa_decode", DECODE, dict(S=0, maxlen=0, ws=None)) == hs.HS_OK
