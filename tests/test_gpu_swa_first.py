@@ -563,6 +563,45 @@ def test_a_window_past_the_documents_takes_the_same_kernels():
         assert all(torch.equal(a, b) for a, b in zip(g, grads[0]))
 
 
+def test_a_band_past_its_limit():
+    """P and dS of every key would take more than the workspace may: the passes that
+    compute them again, for the last rows and the keys that only those attend."""
+    T, W, F, n = 8192, 2100, 4, 300
+    size = lambda W: hs.workspace_size(hs.HS_OP_SWA_FIRST_MQA_BWD, T, 1, T, 64, 64, 64, BF16, W + F)
+    assert size(W) < 2 ** 30 < 2 ** 31 < size(1500)
+    inp, dout = _inputs([T], 64, 64, 64, BF16, 30)
+    args = (inp.cu_seqlens, T, W, F)
+    out, lse = hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink)
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink)
+    assert hs.last_path() == hs.HS_PATH_MMA
+    hs.poll_status()
+    rows = slice(T - n, T)
+    keys = torch.cat([torch.arange(F, device=DEV), torch.arange(T - n - W, T, device=DEV)])
+    t = torch.arange(T - n, T, device=DEV)[:, None]
+    mask = (keys <= t) & ((keys > t - W) | (keys < F))
+    ref = A.backward(inp.q[rows], inp.k[keys], inp.v[keys], out[rows], lse[rows], dout[rows], mask, None, 64 ** -0.5,
+                     BF16)
+    A.check(g[0][rows], *ref["dq"], "dq")
+    for i, name in ((1, "dk"), (2, "dv")):
+        A.check(g[i][rows], *(x[F + W:] for x in ref[name]), name)
+    # the sink's gradient from every row
+    terms = torch.exp(inp.sink.double() - lse.double()) * (dout.double() * out.double()).sum(-1)
+    u = 2.0 ** -20 * (1 + lse.abs() + inp.sink.abs()) + (T + 64) * 2.0 ** -23
+    size = (torch.exp(inp.sink.double() - lse.double()) * (dout.double() * out.double()).abs().sum(-1))
+    A.check(g[3], -terms.sum(0), (u * size).sum(0), "dsink")
+
+
+def test_no_tokens_through_the_c_call():
+    """dsink is the one output with elements."""
+    dsink, p = torch.full((64,), 7.0, device=DEV), torch.zeros(64, device=DEV)
+    at = ctypes.c_void_p(p.data_ptr())
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    st = hs.lib().hs_swa_first_mqa_bwd(at, 64 * 576, 576, at, 576, at, 512, at, 0, 0, 0, 64, 576, 512, hs.HS_BF16, 0.0,
+                                       16, 2, at, at, at, at, at, at, at, ctypes.c_void_p(dsink.data_ptr()), None, 0,
+                                       stream)
+    assert st == hs.HS_OK and not dsink.any()
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
