@@ -74,6 +74,11 @@ struct Walk {
   __device__ __forceinline__ Walk(const Docs& docs, int first_pair, int pairs)
       : d(docs), pair(first_pair), step(pairs), half(0) {}
   __device__ __forceinline__ bool next(Pass& p, int* status) {
+    return next(p, status, [](int) {});
+  }
+  // bad(t): for a token in no (valid) document, which no pass has.
+  template <typename Bad>
+  __device__ __forceinline__ bool next(Pass& p, int* status, Bad bad) {
     while (2 * pair + half < d.T) {
       const int t = 2 * pair + half;
       int bos, eos;
@@ -87,7 +92,10 @@ struct Walk {
       } else {
         half = 1;
       }
-      if (!ok) continue;
+      if (!ok) {
+        bad(t);
+        continue;
+      }
       p.bos = bos;
       p.wlo = max(bos, t - d.window + 1);
       p.nw = t + (both ? 1 : 0) - p.wlo + 1;

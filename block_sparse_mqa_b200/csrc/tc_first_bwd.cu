@@ -13,7 +13,9 @@
 // rounding the products need anyway) into a band in the workspace:
 //   band[t][h][c] is key base(t) + c, base(t) = (t & ~7) - Wp, c < bw
 // (Wp: window - 1 up to a multiple of 8; bw: Wp + 8 up to one of 16), and behind
-// it the first tokens' columns, key bos + c - bw.  Everything outside a token's key set is written as 0.
+// it the first tokens' columns, key bos + c - bw.  Everything outside a token's
+// key set is written as 0, and so is the whole row of a token in no valid document:
+// the key pass takes every token of a chunk.
 // The key-major pass is then a plain product over the band: a tile's 256 keys
 // are columns base-shifted per token, which a TMA box fetches for any token;
 // columns left or right of the band read as 0, so documents and window edges
@@ -224,7 +226,18 @@ query_pass(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUt
       __syncwarp();
       if (lane == 0) arrive_leader(bar);
     };
-    while (ok && walk.next(ps, nullptr)) {
+    auto no_document = [&](int t) {
+      if (rank != 0) return;
+      const int units = (p.band.bw + p.band.fp) / 8;
+      for (int e = tid; e < kH * units; e += 256) {
+        const int64_t at = ((int64_t)t * kH + e / units) * p.band.stride + e % units * 8;
+        *reinterpret_cast<uint4*>(p.pband + at) = make_uint4(0u, 0u, 0u, 0u);
+        *reinterpret_cast<uint4*>(p.sband + at) = make_uint4(0u, 0u, 0u, 0u);
+      }
+      if (tid < kH) p.dsink_part[(int64_t)t * kH + tid] = 0.f;
+      if (tid == 0) p.spoiled[t] = p.spoiled_keys[t] = 0;
+    };
+    while (ok && walk.next(ps, nullptr, no_document)) {
       const Tiles tl(ps, p.band);
       const bool act = ps.active(rank);
       const int t = ps.token(rank);
@@ -684,7 +697,10 @@ struct Jobs {
           if (__ldg(p.d.cu + mid) <= t) lo = mid; else hi = mid;
         }
         const int bos = __ldg(p.d.cu + lo), eos = __ldg(p.d.cu + lo + 1);
-        if (bos < 0 || bos > t || eos <= t) break;  // malformed: pass A reports it
+        if (bos < 0 || bos > t || eos <= t) {  // in no document: pass A reports it
+          ++t;
+          continue;
+        }
         const int from = max(t, bos + p.band.window), to = min(c1, eos);
         t = to;
         if (from >= to) continue;  // every token's window reaches the document's start

@@ -602,6 +602,38 @@ def test_no_tokens_through_the_c_call():
     assert st == hs.HS_OK and not dsink.any()
 
 
+@pytest.mark.parametrize("W", [8, 400])
+@pytest.mark.parametrize("cu,most,good", [([0, 400, 500], 400, [(0, 400), (400, 500)]),  # the last 28 rows in none
+                                          ([5, 400, 528], 400, [(5, 400), (400, 528)]),  # the first 5 in none
+                                          ([0, 151, 451, 528], 200, [(0, 151), (451, 528)])])  # one past the bound
+def test_rows_in_no_document_give_nothing_to_the_others(W, cu, most, good):
+    """Their part of the workspace is never taken for probabilities: dq, dk, dv of the
+    documents that are right, and dsink from those rows alone."""
+    F, T, stale = 2, 528, 0x3C  # bf16 0x3C3C is 0.0115
+    inp, dout = _inputs([T], 64, 64, 512, BF16, 31)
+    args = (torch.tensor(cu, device=DEV, dtype=torch.int32), most, W, F)
+    out, lse = torch.zeros((T, 64, 512), device=DEV, dtype=BF16), torch.full((T, 64), 1.0, device=DEV)
+    hs.hs_swa_first_mqa_fwd(inp.q, inp.k, inp.v, *args, inp.sink, out=out, lse=lse)
+    with pytest.raises(hs.HSError):
+        hs.poll_status()
+    need = hs.workspace_size(hs.HS_OP_SWA_FIRST_MQA_BWD, T, len(cu) - 1, most, 64, 64, 512, BF16, min(W, most) + F)
+    ws = torch.full((need,), stale, dtype=torch.uint8, device=DEV)
+    g = hs.hs_swa_first_mqa_bwd(inp.q, inp.k, inp.v, *args, out, lse, dout, inp.sink, workspace=ws)
+    assert hs.last_path() == hs.HS_PATH_MMA
+    with pytest.raises(hs.HSError) as e:
+        hs.poll_status()
+    assert e.value.status == hs.HS_ERR_INVALID_ARG
+    dsink, room = torch.zeros(64, device=DEV, dtype=torch.float64), 0.0
+    for a, b in good:
+        r = slice(a, b)
+        ref = A.backward(inp.q[r], inp.k[r], inp.v[r], out[r], lse[r], dout[r], A.mask_of([0, b - a], W, F, DEV),
+                         inp.sink, 64 ** -0.5, BF16)
+        for x, name in zip(g, ("dq", "dk", "dv")):
+            A.check(x[r], *ref[name], name)
+        dsink, room = dsink + ref["dsink"][0], room + ref["dsink"][1]
+    A.check(g[3], dsink, room, "dsink")
+
+
 def test_without_tensor_cores():
     """The CUDA-core kernels at the shape that normally does not reach them."""
     hs.set_force_simt(True)
