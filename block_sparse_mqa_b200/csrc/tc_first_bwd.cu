@@ -32,8 +32,9 @@
 //   reduce  adds a key's partial sums in order, scales, rounds once
 // Results are deterministic.  All waits are bounded (HS_ERR_TIMEOUT).
 //
-// Measured (Dk 576 / Dv 512, 4096 tokens, window 512 + 4 first, in a graph): the
-// whole backward 1.06 ms, 659 TFLOP/s, 0.40 of a cuBLAS matmul's rate (pass A
+// Measured (Dk 576 / Dv 512, 4096 tokens, window 512 + 4 first, in a graph, full
+// clock): the whole backward 1.08 ms, 648 TFLOP/s, 0.39 of a cuBLAS matmul's rate
+// (1.27 ms in a long run under the power cap, 0.39 of that rate too; pass A
 // with delta 0.61 ms, pass B 0.41 ms, reduction 33 us); the passes of
 // tc_bwd_dq.cu and tc_bwd_dkdv.cu, which recompute P and dS for dk and dv and
 // take one token per CTA, need 3.81 ms for the same and less workspace (333

@@ -32,14 +32,15 @@
 // next one begins.  The running maximum is raised only past 2^8.
 // All waits are bounded (HS_ERR_TIMEOUT).
 //
-// Measured (Dk 576 / Dv 512, window 512 + 4 first, in a graph): 4096 tokens 276
-// us, 1000 TFLOP/s, 0.60 of a cuBLAS matmul's rate; the window kernel with one
-// token per CTA (tc_attention.cu) takes 376 us for its 512 keys.  What bounds it
-// is the operands' way from L2 (11 TB/s into the SMs, 112 KB of ring under way
-// per SM) and the ~85 cycles between two MMAs of one issuing warp.  Dk 192 / Dv
-// 128, window 1024 + 64: 8192 tokens 487 us, 672 TFLOP/s, bound by the softmax
-// (3.7K cycles a tile, a third of it exponentials).  The CUDA-core kernel takes 18.5 ms for 512
-// tokens that take 37 us here, and 21 us for 8 that take 10.
+// Measured (Dk 576 / Dv 512, window 512 + 4 first, in a graph, full clock): 4096 tokens
+// 280 us, 986 TFLOP/s, 0.60 of a cuBLAS matmul's rate (327 us and 0.60 of that rate in
+// a long run under the power cap); the window kernel with one token per CTA
+// (tc_attention.cu) takes 376 us for its 512 keys.  What bounds it is the operands'
+// way from L2 (11 TB/s into the SMs, 112 KB of ring under way per SM) and the ~85
+// cycles between two MMAs of one issuing warp.  Dk 192 / Dv 128, window 1024 + 64:
+// 8192 tokens 491 us, 666 TFLOP/s, bound by the softmax (3.7K cycles a tile, a third
+// of it exponentials).  The CUDA-core kernel takes 18.5 ms for 512 tokens that take
+// 37 us here, and 21 us for 8 that take 10.
 
 #include <math.h>
 

@@ -38,7 +38,7 @@
 // All waits are bounded (HS_ERR_TIMEOUT).
 //
 // Measured (64 heads, Dk 576 / Dv 512 in one plane, in a graph): 64 sequences of
-// ~4900 keys 81 us, 540 TFLOP/s and 1.3 TB/s; 4 sequences of 65536 keys at most 92 us.  A
+// ~4900 keys 84 us, 520 TFLOP/s and 1.25 TB/s; 4 sequences of 65536 keys at most 97 us.  A
 // tile of 128 keys costs ~6.3K cycles (PV 1.7K, then expansion, QK and softmax
 // behind one another in part); ~20 us are prologue, epilogue and the join.
 // The CUDA-core kernel takes 353 us for 8 sequences of 2048 keys at most that
